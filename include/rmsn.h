@@ -319,7 +319,8 @@ int64_t rmsn_small_t_max(void);
  * hanging; the outputs of that call are then incomplete.  This call synchronizes
  * `stream`, reads and clears the current device's error word into *flags (bit 0: a row
  * never landed; bit 1: a stage was never released; bit 2: copies were still in flight
- * when a CTA gave up) and returns RMSN_OK if it was 0, RMSN_ERR_DEVICE_TIMEOUT otherwise.
+ * when a CTA gave up; bit 3: a position, slot, page id or length outside its table) and
+ * returns RMSN_OK if it was 0, RMSN_ERR_DEVICE_TIMEOUT otherwise.
  * ---------------------------------------------------------------------------------- */
 int rmsn_device_status(rmsn_stream_t stream, unsigned* flags);
 
@@ -371,6 +372,158 @@ int rmsn_selftest_wait_timeout(uint64_t limit_ns, rmsn_stream_t stream);
 int rmsnorm_bwd_noalloc(const void* dy, const void* x, int x_dtype, const void* w, int w_dtype,
                         const float* rstd, void* dx, float* dw, int64_t T, int64_t H,
                         int compensated, rmsn_stream_t stream);
+
+/* ====================================================================================
+ * The norms inside attention: queries and keys normed per head and rotated by position, for
+ * training (forward, backward) and for serving (the new K and V go to a paged cache in 4 bits
+ * in the same pass; attention over that cache).  The conventions above hold; in addition
+ *
+ *   - A row is one head of one token, D elements with unit stride; D is a multiple of 16, 16
+ *     to 256 (64, 128 or 256 where the cache takes part).
+ *   - Tokens lie on two axes, batch and token, so that [B, S, H, D] and [B, H, S, D] tensors,
+ *     views into a fused projection's output and plain [T, H, D] (B = 1) are all described by
+ *     strides.  B * T is below 2^31.
+ *   - Device-side indices (positions, slots, page ids, lengths) cannot be checked on the host.
+ *     The kernels check each one: one that is out of range is not followed, sets bit 3 of the
+ *     device error word (rmsn_device_status), and what is then done is stated per call.
+ * ==================================================================================== */
+
+/* The heads of one tensor.  Strides in elements, >= 0; every stride of an axis longer than 1
+ * is a multiple of 16 bytes.  Outputs must not overlap themselves; an output may be an input's
+ * own memory with the same strides (in place), and must not overlap it in another way. */
+typedef struct {
+    void* data;           /* first element, 16-byte aligned */
+    int64_t batch_stride; /* not looked at where B = 1 */
+    int64_t token_stride;
+    int64_t head_stride;
+    int64_t heads;        /* 1 .. 4096 */
+} rmsn_heads_t;
+
+/* The rotation.  Dims below rot_dim (a multiple of 16, 16 .. D) turn in pairs, the others pass:
+ * pair i < rot_dim/2 is dims (i, i + rot_dim/2), or (2i, 2i + 1) where `neighbours` is set, and
+ *   (a, b) -> (a cos - b sin, b cos + a sin)   with cos, sin at [position][i].  A table row is
+ * any pair of numbers, so scaled or otherwise modified angles need nothing else. */
+typedef struct {
+    const float* cos; /* [rows, rot_dim/2], contiguous, 16-byte aligned */
+    const float* sin;
+    int64_t rows;     /* >= 1 */
+    int64_t rot_dim;
+    int neighbours;
+    const int64_t* positions; /* [B, T] by strides (0 broadcasts), 8-byte aligned */
+    int64_t pos_batch_stride; /* not looked at where B = 1 */
+    int64_t pos_token_stride;
+} rmsn_rope_t;
+
+/* ------------------------------------------------------------------------------------
+ * qk_norm_rope_fwd -- y = rotate((x * rstd) * w) for every head of q (with wq) and k (with wk),
+ * rstd = 1/sqrt(mean(x^2) + eps) over the head's D elements, FP32, one rounding to x_dtype.
+ *
+ *   q, k, q_out, k_out  tensors of x_dtype; heads of q_out as q, of k_out as k
+ *   wq, wk              [D] of w_dtype, shared by all heads
+ * A token whose position is not a table row is left out: its output rows stay as they were and
+ * the error word's bit 3 is set.  B * T == 0 writes nothing.
+ * ---------------------------------------------------------------------------------- */
+int qk_norm_rope_fwd(const rmsn_heads_t* q, const rmsn_heads_t* k, int x_dtype, const void* wq,
+                     const void* wk, int w_dtype, const rmsn_rope_t* rope,
+                     const rmsn_heads_t* q_out, const rmsn_heads_t* k_out, int64_t B, int64_t T,
+                     int64_t D, float eps, rmsn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * qk_norm_rope_bwd -- the gradients of qk_norm_rope_fwd.
+ *
+ *   gq, gk    gradients of q_out and k_out (x_dtype)
+ *   q, k      the forward's inputs; rstd is formed from them again (nothing is saved)
+ *   dq, dk    gradients of q and k (x_dtype); may be gq, gk or q, k in place
+ *   dwq, dwk  [D] fp32, overwritten: sums over all tokens and heads, in a fixed order, kept as
+ *             TwoSum (high, low) pairs and rounded once; the same bits on every run
+ *   workspace at least qk_norm_rope_bwd_workspace_bytes(D, device) bytes, 16-byte aligned;
+ *             contents do not matter.  Calls that may overlap in time need one each.
+ * A token whose position is not a table row: dq and dk rows stay as they were, nothing is added
+ * to dwq and dwk, bit 3 is set.  B * T == 0 zeroes dwq and dwk.
+ * ---------------------------------------------------------------------------------- */
+size_t qk_norm_rope_bwd_workspace_bytes(int64_t D, int device);
+
+int qk_norm_rope_bwd(const rmsn_heads_t* gq, const rmsn_heads_t* gk, const rmsn_heads_t* q,
+                     const rmsn_heads_t* k, int x_dtype, const void* wq, const void* wk,
+                     int w_dtype, const rmsn_rope_t* rope, const rmsn_heads_t* dq,
+                     const rmsn_heads_t* dk, float* dwq, float* dwk, int64_t B, int64_t T,
+                     int64_t D, float eps, void* workspace, size_t workspace_bytes,
+                     rmsn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The 4-bit cache: [pages][kv_heads][page_size / 16] records of 20 * D bytes, 16-byte aligned,
+ * contiguous; page_size a multiple of 16; fewer than 2^31 records.  A record holds K and V of
+ * 16 consecutive tokens of one head: 4-bit codes, and per group of 32 dims a bf16 scale s and a
+ * bf16 minimum z; a code c stands for c * s + z.  With x the group's bf16 values,
+ *   z = min x,  s = bf16(max x / 15 - min x / 15),  c = clamp(rint((x - z) / s), 0, 15)
+ * in IEEE FP32 (s = 0: c = 0; values up to half of the type's range).  A group with a NaN or
+ * an infinity reads back as NaN.  The order inside a record is the library's
+ * (csrc/rmsn_kv4_layout.h).  A token's slot is page * page_size + place in the page; tokens
+ * are stored independently, so any may be overwritten alone.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+    void* data;
+    int64_t pages, kv_heads, page_size;
+} rmsn_kv4_t;
+
+/* ------------------------------------------------------------------------------------
+ * qk_norm_rope_kv4_append -- the serving form of qk_norm_rope_fwd: q is normed, rotated and
+ * written to q_out; k is normed, rotated, rounded to bf16 and stored to the cache in 4 bits; v
+ * is stored as it is.  All in bf16; B = 1 (tokens [T, heads, D] by strides).
+ *
+ *   slots  [T] where each token's K and V go.  A token with a negative slot is padding: nothing
+ *          is read or written for it, q_out included.  A slot beyond the cache, or a position
+ *          that is not a table row: likewise, and bit 3 is set.  Two tokens with one slot in a
+ *          call leave that slot with an unspecified mixture of both.
+ *   q_out  may be q itself.
+ * ---------------------------------------------------------------------------------- */
+int qk_norm_rope_kv4_append(const rmsn_heads_t* q, const rmsn_heads_t* k, const rmsn_heads_t* v,
+                            const void* wq, const void* wk, int w_dtype, const rmsn_rope_t* rope,
+                            const rmsn_heads_t* q_out, const rmsn_kv4_t* cache,
+                            const int64_t* slots, int64_t T, int64_t D, float eps,
+                            rmsn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * kv4_read -- K and V of any slots as bf16 (c * s + z in FP32, rounded once): the inverse of
+ * the append, e.g. for a dense attention over a cached prefix.  k and v are outputs of
+ * [T, kv_heads, D] by strides.  Rows of a negative slot stay as they were; so do those of a
+ * slot beyond the cache, which sets bit 3.
+ * ---------------------------------------------------------------------------------- */
+int kv4_read(const rmsn_kv4_t* cache, const int64_t* slots, const rmsn_heads_t* k,
+             const rmsn_heads_t* v, int64_t T, int64_t D, rmsn_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * kv4_attention -- attention of the last tokens of each sequence over the 4-bit cache:
+ *   out = softmax(scale * q K^T) V,  lse = log(sum exp(scale * q K^T))
+ * Sequence b has kv_lens[b] cached tokens, in the pages page_table[b][0], [1], ... of page_size
+ * tokens each, and the query tokens cu_q[b] .. cu_q[b+1]-1 (cu_q NULL: T = seqs, one each).
+ * The query tokens are the sequence's last: query i of n sees the first kv_lens[b] - n + 1 + i
+ * tokens.  A query that sees none gives out = 0, lse = -inf.
+ *
+ *   q, out    bf16 [T, heads, D] by strides; heads a multiple of the cache's kv_heads (query
+ *             head i reads kv head i / (heads / kv_heads)); out must not overlap q
+ *   lse       [T, heads] fp32, contiguous, or NULL
+ *   page_table  int32 [seqs, table_width], rows table_stride apart; entries behind a
+ *             sequence's length are not read
+ *   kv_lens   int32 [seqs]; less than 0 counts as 0, more than table_width * page_size as that
+ *             (and sets bit 3)
+ *   cu_q      int32 [seqs + 1], rising, within 0 .. T; rows of out and lse that no sequence
+ *             has stay as they were
+ *   max_q     >= 1: about how many query tokens a sequence has at most.  It chooses how many
+ *             are worked on together; results are right for any value.
+ *   workspace at least kv4_attention_workspace_bytes(seqs, D, device) bytes, 16-byte aligned;
+ *             contents do not matter.  Calls that may overlap in time need one each.
+ * A page id outside the cache: its tokens are left out and bit 3 is set.  What a cached token
+ * holds reaches only the queries that see it, NaN included.  The work split, and so the
+ * rounding, depends on all lengths of the call; the same call gives the same bits every time.
+ * ---------------------------------------------------------------------------------- */
+size_t kv4_attention_workspace_bytes(int64_t seqs, int64_t D, int device);
+
+int kv4_attention(const rmsn_heads_t* q, const rmsn_kv4_t* cache, const int32_t* page_table,
+                  int64_t table_width, int64_t table_stride, const int32_t* kv_lens,
+                  const int32_t* cu_q, int64_t max_q, int64_t seqs, int64_t T, int64_t D,
+                  float scale, const rmsn_heads_t* out, float* lse, void* workspace,
+                  size_t workspace_bytes, rmsn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -15,12 +15,20 @@ import threading
 
 import torch
 
+from . import attn as _attn
+from .attn import (  # noqa: F401  (public entry points)
+    KV4_BLOCK, KV4_GROUP, kv4_attention, kv4_attention_workspace_bytes, kv4_cache_shape, kv4_read,
+    qk_norm_rope_bwd, qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_fwd, qk_norm_rope_kv4_append)
+
 __all__ = [
     "RMSN_F32", "RMSN_BF16", "RMSN_MAX_H", "RmsnError", "library_path", "load_library",
     "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
     "rmsnorm_fwd_residual", "rmsnorm_bwd_residual",
     "fused_add_rmsnorm_fp8_block_quant", "rmsn_status_string", "rmsn_plan", "rmsn_set_policy",
     "rmsn_device_status", "rmsn_set_small_t_max", "rmsn_small_t_max", "rmsn_selftest_wait_timeout",
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes",
+    "qk_norm_rope_kv4_append", "kv4_cache_shape", "kv4_read", "kv4_attention",
+    "kv4_attention_workspace_bytes", "KV4_GROUP", "KV4_BLOCK",
     "OP_FWD", "OP_BWD", "OP_FUSED_QUANT", "OP_FWD_RESIDUAL", "OP_BWD_RESIDUAL",
 ]
 
@@ -103,6 +111,7 @@ def load_library():
         L.rmsnorm_bwd_noalloc.restype = ctypes.c_int
         L.rmsnorm_bwd_noalloc.argtypes = [_vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
                                           _vp, _i64, _i64, ctypes.c_int, _vp]
+        _attn.declare(L)
         _lib = L
         return _lib
 

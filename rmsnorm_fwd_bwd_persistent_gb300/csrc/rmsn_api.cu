@@ -313,6 +313,20 @@ int plan_current(int op, int64_t T, int64_t H, int x_dt, int w_dt, Launch* L, in
 
 namespace rmsn {
 
+int device_facts(int* sms, unsigned** err, uint64_t* limit_ns) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return RMSN_ERR_CUDA;
+    }
+    const DevProps* p = props_of(dev);
+    if (!p) return RMSN_ERR_CUDA;
+    *sms = p->sms;
+    *err = error_word(dev);
+    *limit_ns = kWaitLimitNs;
+    return *err ? RMSN_OK : RMSN_ERR_CUDA;
+}
+
 // Self-test of the bounded wait: one thread waits on an mbarrier that expects an arrival
 // nobody makes (no copy is in flight), gives up after `limit_ns`, and reports it through
 // the error word exactly as a pipeline wait does.

@@ -63,4 +63,8 @@ cudaError_t launch_fused(const Launch& L, const void* x, void* residual, const v
 // waves.  Cached per device and kernel.
 cudaError_t fit_grid(const void* kernel, const Launch& L, int threads, int64_t* grid);
 
+// Multiprocessors and device error word of the current device, and the time limit of every
+// wait; returns a rmsn_status.
+int device_facts(int* sms, unsigned** err, uint64_t* limit_ns);
+
 }  // namespace rmsn

@@ -1,0 +1,248 @@
+// rmsn_qk.cuh -- the row geometry shared by the per-head norm + rotation kernels.
+//
+// A row is one head of one token: D elements, D a multiple of 16, at most 256.  LPR lanes
+// (the power of two >= D/16) share a row, so a warp works on RPW = 32/LPR rows at a time;
+// lane l of a row holds 16 elements as two vectors of 8, chosen so that both members of every
+// rotated pair are in the same lane and no exchange between lanes is needed:
+//   half pairs (i, i + rd/2):  lanes l < rd/16 hold dims [8l, 8l+8) and rd/2 + [8l, 8l+8)
+//   neighbours (2i, 2i+1):     dims [16l, 16l+16)
+//   the part that is not rotated (dims >= rd): dims [16l, 16l+16), with cos = 1, sin = 0
+// In both styles lane l needs the angles [8l, 8l+8) of its token's table row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rmsn_device.cuh"
+
+namespace rmsn {
+
+constexpr unsigned ERR_INDEX = 8u;  // a position, slot or page outside its table
+
+// Eight elements as they are in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        a = __ldg(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&f)[8]) const { Elem<__nv_bfloat16>::unpack(a, f); }
+    __device__ __forceinline__ void set(const float (&f)[8]) { a = Elem<__nv_bfloat16>::pack(f); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const {
+        *reinterpret_cast<uint4*>(p) = a;
+    }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+};
+
+// A lane's place in its row, and the angles and weights that go with it.
+template <bool NEIGHBOURS>
+struct RowLane {
+    int off0, off1;  // first dims of its two vectors
+    bool turns;      // holds rotated dims
+
+    __device__ __forceinline__ void init(int l, int rd) {
+        turns = 16 * l < rd;
+        if (!NEIGHBOURS && turns) {
+            off0 = 8 * l;
+            off1 = rd / 2 + 8 * l;
+        } else {
+            off0 = 16 * l;
+            off1 = 16 * l + 8;
+        }
+    }
+};
+
+// Angles of one token: cos and sin of the lane's eight pairs.
+struct Angles {
+    float c[8], s[8];
+    __device__ __forceinline__ void identity() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    }
+    __device__ __forceinline__ void load(const float* cosp, const float* sinp) {
+        const float4* p = reinterpret_cast<const float4*>(cosp);
+        const float4* q = reinterpret_cast<const float4*>(sinp);
+        const float4 c0 = __ldg(p), c1 = __ldg(p + 1), s0 = __ldg(q), s1 = __ldg(q + 1);
+        c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w;
+        c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+        s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w;
+        s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
+    }
+};
+
+// Rotates the lane's 16 elements (u: first vector, v: second) by its angles, in place;
+// TRANSPOSE rotates back (the gradient's direction).
+template <bool NEIGHBOURS, bool TRANSPOSE>
+__device__ __forceinline__ void rotate(float (&u)[8], float (&v)[8], const Angles& t) {
+    auto turn = [](float& a, float& b, float c, float s) {
+        const float x = a, y = b;
+        a = TRANSPOSE ? fmaf(y, s, x * c) : fmaf(-y, s, x * c);
+        b = TRANSPOSE ? fmaf(-x, s, y * c) : fmaf(x, s, y * c);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (NEIGHBOURS) {
+            if (i < 4)
+                turn(u[2 * i], u[2 * i + 1], t.c[i], t.s[i]);
+            else
+                turn(v[2 * i - 8], v[2 * i - 7], t.c[i], t.s[i]);
+        } else {
+            turn(u[i], v[i], t.c[i], t.s[i]);
+        }
+    }
+}
+
+// Eight weights as FP32.
+__device__ __forceinline__ void load_w8(const void* w, int bf16, int off, float (&f)[8]) {
+    if (bf16) {
+        Raw8<__nv_bfloat16> r;
+        r.load(static_cast<const __nv_bfloat16*>(w) + off);
+        r.get(f);
+    } else {
+        Raw8<float> r;
+        r.load(static_cast<const float*>(w) + off);
+        r.get(f);
+    }
+}
+
+// Sum over the LPR lanes of a row (every lane gets the same bits).
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// 1/sqrt(ss/D + eps), IEEE operations (rd: 1/D rounded is not used, the mean is a division).
+__device__ __forceinline__ float row_rstd(float ss, float D, float eps) {
+    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, D), eps)));
+}
+
+// One operand of the kernels: the rows of q, k or v in memory.  Strides in elements.
+struct Heads {
+    void* p;
+    int64_t sb, st, sh;
+    template <typename T>
+    __device__ __forceinline__ T* row(int b, int t) const {
+        return static_cast<T*>(p) + b * sb + t * st;
+    }
+};
+
+// How a warp's rows lie over tokens and heads: hpw heads (a power of two) of tpw tokens at a
+// time, `chunks` such steps for all heads of the tokens, split into `parts` units of work.
+struct Span {
+    int heads, log_hpw, chunks, per_part, parts;
+};
+
+struct Rope {
+    const float* cos;
+    const float* sin;
+    const int64_t* pos;
+    int64_t pos_sb, pos_st, rows;
+    int rd;
+};
+
+// The token of one row of a warp: index, position, and whether its row is worked on.
+struct Token {
+    int b, t;
+    bool ok;
+    int64_t pos;
+};
+
+__device__ __forceinline__ Token find_token(int tok, int tokens, int T, const Rope& rope,
+                                            unsigned* err, bool report) {
+    Token k;
+    k.ok = tok < tokens;
+    const int c = k.ok ? tok : 0;
+    k.b = tokens == T ? 0 : c / T;
+    k.t = c - k.b * T;
+    k.pos = __ldg(rope.pos + k.b * rope.pos_sb + k.t * rope.pos_st);
+    if (k.ok && (k.pos < 0 || k.pos >= rope.rows)) {
+        if (report) atomicOr(err, ERR_INDEX);
+        k.ok = false;
+    }
+    return k;
+}
+
+// Lanes per row for a head of D elements.
+inline int lanes_per_row(int D) {
+    int n = 1;
+    while (16 * n < D) n *= 2;
+    return n;
+}
+
+// The rows of one side over a warp: as many heads of a token as fit (a power of two), the
+// rest of the warp's rows on the next tokens.
+inline Span make_span(int heads, int rpw, int per_part) {
+    Span s{};
+    s.heads = heads;
+    while ((2 << s.log_hpw) <= rpw && (1 << s.log_hpw) < heads) ++s.log_hpw;
+    s.chunks = (heads + (1 << s.log_hpw) - 1) >> s.log_hpw;
+    s.per_part = per_part < s.chunks ? per_part : s.chunks;
+    s.parts = (s.chunks + s.per_part - 1) / s.per_part;
+    return s;
+}
+
+inline int64_t groups_of(int64_t tokens, const Span& s, int rpw) {
+    const int tpw = rpw >> s.log_hpw;
+    return (tokens + tpw - 1) / tpw;
+}
+
+// Chunks per unit of work: the most (8 at first) that still leave about two warps for each
+// of an SM's four schedulers.
+inline int pick_per_part(const int* heads, int sides, int64_t tokens, int rpw, int sms) {
+    int per = 8;
+    for (; per > 1; per /= 2) {
+        int64_t units = 0;
+        for (int i = 0; i < sides; ++i) {
+            const Span s = make_span(heads[i], rpw, per);
+            units += groups_of(tokens, s, rpw) * s.parts;
+        }
+        if (units >= (int64_t)sms * 8) break;
+    }
+    return per;
+}
+
+// A checked call of the norm + rotation (x -> y, or with ws the backward: g, x -> y = dx).
+struct QkCall {
+    Heads x[2], y[2], g[2];
+    const void* w[2];
+    float* dw[2];
+    int heads[2];
+    Rope rope;
+    float* ws;
+    unsigned* err;
+    int64_t tokens, T;
+    int D, x_dt, w_dt, sms;
+    bool neighbours;
+    float eps;
+};
+constexpr int kQkBwdCtasPerSm = 4;  // the backward's persistent CTAs (its workspace's size)
+
+cudaError_t launch_qk(const QkCall& c, cudaStream_t s);
+
+}  // namespace rmsn
