@@ -3,31 +3,36 @@
 //   o = softmax(scale q K^T) V,  lse = log sum exp;  K = c s + z per group of 32 dims
 //
 // What bounds it: the cache is read once (1.25 D bytes per token and head), and every code
-// has to reach a matrix instruction as a 16-bit number; with one query token per sequence the
-// second takes more issue slots than the first takes memory time, so the work per code is what
-// the layout and the arithmetic below keep small.
+// has to reach a matrix instruction as a 16-bit number.  The logic pipe that takes codes out of
+// their words issues every other cycle, so the work per code is what the layout and the
+// arithmetic below keep small.
 //
-// Mathematics.  The scores are formed transposed, S^T = K q^T, with 16 tokens as the M rows and
-// 8 (query token, head) columns of one kv head as N, so no row of the matrix instruction is
-// padding when a kv head serves 8 query heads.  A matrix step of 16 dims stays inside one group
-// of 32, so the scale and minimum come after the product, in FP32:
-//   q . k = sum_j ( s_j (c . q)_j + z_j (sum of q)_j )
-// and the codes themselves are the operand: a nibble masked out of its word is the binary16
+// Scores.  They are formed transposed, S^T = K q^T, with 16 tokens as the M rows and 8 (query
+// token, head) columns of one kv head as N, so no row of the matrix instruction is padding when
+// a kv head serves 8 query heads.  A matrix step of 16 dims stays inside one group of 32, so the
+// scale comes after the product, in FP32, and the minima are a product of their own:
+//   q . k = sum_j s_j (c . q)_j + sum_j z_j (sum of q)_j
+// The codes themselves are the operand: a nibble masked out of its word is the binary16
 // subnormal c 2^-24 (or, four bits up, c 2^-20: those dims of q are divided by 16), so one AND
-// makes two operands; q is scaled by a power of two to use binary16's range, which is exact for
-// its bf16 values down to 2^-17 of the row's largest.  The softmax runs over one pass with a running
-// maximum per column that moves only when a score exceeds it by 2^8 (the probabilities of up
-// to 256 are harmless in bf16 and FP32), so most blocks need one vote instead of a reduction.
-// O^T = V^T P^T takes the probabilities transposed by movmatrix, rounded to bf16, and V as
-// bf16 values c s + z (c exact by 128 + c - 128 in bf16, one FMA rounding).  Sums, maxima and
-// outputs are FP32.
+// makes two operands.  q is scaled by a power of two to use binary16's range, which is exact for
+// its bf16 values down to 2^-17 of the row's largest.  The sums of q enter as three bf16 terms
+// (24 bits) against the bf16 minima as they lie in the cache.
 //
-// Work split.  Blocks of 16 tokens of all (sequence, kv head) items form one line of units that
-// is cut into equal shares, one per CTA, so ragged batches and single long sequences load all
-// SMs alike; a CTA's four warps take the blocks of an item in turn, each streaming its own
-// blocks through a ring in shared memory (bulk copies of a whole record), and merge at the
-// item's end.  An item that lies in several CTAs leaves partial sums in the workspace, which
-// kv4_combine_kernel adds in CTA order: results do not depend on timing.
+// Softmax.  One pass with a running reference per column, which moves only when a score exceeds
+// it by 2^8, so most blocks need one vote instead of a reduction.
+//
+// Values.  O^T = V^T P^T takes the probabilities (binary16, at most 2^8) transposed by
+// movmatrix, and V as binary16 values c s + z by one FMA on the masked codes.  binary16 keeps 11
+// bits where bf16 keeps 8 (with bf16 the result was 2.8e-3 off instead of 1.7e-3, of which 1.7e-3
+// is the output's own rounding); its range is given by a running power of two per group, 2^k,
+// that rises when a scale or minimum needs it.  Sums, references and outputs are FP32.
+//
+// Work split.  Units of 32 tokens of all (sequence, kv head) items form one line that is cut
+// into equal shares, one per CTA, so ragged batches and single long sequences load all SMs
+// alike; a CTA's four warps take the units of an item in turn, each streaming its own through
+// a ring in shared memory (bulk copies of whole records), and merge at the item's end.  An item
+// that lies in several CTAs leaves partial sums in the workspace, which kv4_combine_kernel adds
+// in CTA order: results do not depend on timing.
 #include <cfloat>
 
 #include "rmsn_internal.h"
@@ -41,9 +46,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;      // at most (sizes the workspace)
-constexpr int kMinShare = 8;       // least blocks per CTA: two for each warp
+constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
+constexpr int kMinShare = kWarps;  // least units per CTA: one for each warp
 
-__host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : 3; }
+// Ring stages of one unit per warp: about 64 KiB in flight per SM.
+__host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
 struct Args {
     const bf16* q;
@@ -67,7 +74,7 @@ struct Args {
 
 // One sequence's share of the problem.
 struct Seq {
-    int q0, n, len, blocks, qblocks;
+    int q0, n, len, units, qblocks;
 };
 
 template <int QC>
@@ -84,7 +91,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool report) {
     const int most = a.table_width * a.nb * kKv4Block;
     if (len > most && report) atomicOr(a.err, ERR_INDEX);
     s.len = min(max(len, 0), most);
-    s.blocks = (s.len + kKv4Block - 1) / kKv4Block;
+    s.units = (s.len + kUnit - 1) / kUnit;
     s.qblocks = (s.n * a.group + QC - 1) / QC;
     return s;
 }
@@ -122,12 +129,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return d;
 }
 
-// Two codes (bits 0-3 and 16-19 of x, others masked) times s plus z, as bf16x2.
-__device__ __forceinline__ uint32_t value2(uint32_t x, uint32_t s2, uint32_t z2) {
-    uint32_t v = (x & 0x000f000fu) | 0x43004300u;  // 128 + c in bf16
-    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(v) : "r"(s2), "r"(z2));
-    return v;
+// a b + c in binary16, two at a time.
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 2^e for e in [-126, 127], limited to that range
+__device__ __forceinline__ float pow2(int e) {
+    return __int_as_float((min(max(e, -126), 127) + 127) << 23);
+}
+// exponent e of a finite v > 0 with v < 2^e; -126 for 0 and for what is not finite
+__device__ __forceinline__ int exponent(float v) {
+    const int e = (__float_as_int(v) >> 23) & 255;
+    return e == 255 ? -126 : e - 126;
 }
 
 // N 32-bit words from shared memory in the widest loads.
@@ -157,7 +181,7 @@ struct Smem {
     static constexpr int S = stages_of(D);
     static constexpr int QC = 8 * NT;
     static constexpr int OS = D + 4;  // padded row of the merge buffer
-    uint8_t ring[kWarps][S][20 * D];
+    uint8_t ring[kWarps][S][2 * 20 * D];
     float o[kWarps][QC][OS];
     float m[kWarps][QC], l[kWarps][QC];
     uint64_t full[kWarps][S];
@@ -168,19 +192,24 @@ struct Smem {
 // The columns' state of one warp over one item.
 template <int D, int NT>
 struct Warp {
-    static constexpr int NG = D / 32;  // groups, and K words per lane and token
-    static constexpr int VW = D / 64;  // V words per lane and token
-    static constexpr int MT = D / 16;  // M tiles of O^T
-    uint32_t qf[NT][NG][4];            // q as binary16 pairs, column g
-    float qz[NT][NG][2];               // (sum of q)_j, columns 2t and 2t + 1, log2 units
-    float f[NT][2];                    // factor of the code products, log2 units
-    int lim[NT][2];                    // tokens that the column sees
-    float o[NT][MT][4];
+    static constexpr int NG = D / 32;   // groups, and K words per lane and token
+    static constexpr int VW = D / 64;   // V words per lane and token
+    static constexpr int MT = D / 16;   // M tiles of O^T
+    static constexpr int NZ = D == 256 ? 2 : 1;  // matrix steps of the minima
+    uint32_t qf[NT][NG][4];             // q as binary16 pairs, column g
+    uint32_t qz[NT][NZ][2];             // sums of q per group, three bf16 terms, column g
+    float f[NT][2];                     // factor of the code products, log2 units
+    int lim[NT][2];                     // tokens that columns 2t and 2t + 1 see
+    float o[NT][MT][4];                 // times 2^k
     float m[NT][2], l[NT][2];
+    int k;                              // of the lane's group of V dims
+    bool first;                         // no unit seen yet
 
     // Loads the item's query rows and resets the sums.
     __device__ __forceinline__ void begin(const Args& a, const Seq& s, int qb, int h, int lane) {
         const int g = lane >> 2, t = lane & 3;
+        first = true;
+        k = -100;  // V below about 2^-100 counts as 0
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int col = (qb * NT + nt) * 8 + g;
@@ -201,11 +230,9 @@ struct Warp {
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            int ex = 0;  // the row's largest becomes 2^14 .. 2^15
-            if (amax > 0.f && amax <= FLT_MAX) {
-                frexpf(amax, &ex);
-                ex -= 15;
-            }
+            // the row's largest becomes 2^14 .. 2^15 (in two factors: the power may be beyond FP32)
+            const int ex = amax > 0.f && amax <= FLT_MAX ? exponent(amax) - 15 : 0;
+            const float p1 = pow2(-ex / 2), p2 = pow2(-ex - -ex / 2);
             float z[NG];
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
@@ -214,25 +241,34 @@ struct Warp {
                 for (int e = 0; e < 8; ++e) z[j] += x[j][e];
                 z[j] += __shfl_xor_sync(0xffffffffu, z[j], 1);
                 z[j] += __shfl_xor_sync(0xffffffffu, z[j], 2);
+                z[j] *= a.scale_log2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int sh = e & 1 ? -ex - 4 : -ex;
-                    const __half2 p = __floats2half2_rn(ldexpf(x[j][e], sh), ldexpf(x[j][e + 4], sh));
-                    qf[nt][j][e] = *reinterpret_cast<const uint32_t*>(&p);
+                    const float d = e & 1 ? 0.0625f : 1.f;
+                    qf[nt][j][e] = pack_f16x2(x[j][e] * p1 * p2 * d, x[j][e + 4] * p1 * p2 * d);
                 }
             }
-            const float fac = ldexpf(a.scale_log2, ex + 24);
+            // z = z0 + z1 + z2 in bf16; step (term, group) of the minima's product
+            auto term = [&](int n, int j) -> uint32_t {
+                float v = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {  // from the lanes of column 2t + c
-                const int src = 8 * t + 4 * c;
-                f[nt][c] = __shfl_sync(0xffffffffu, fac, src);
+                for (int i2 = 0; i2 < NG; ++i2) v = i2 == j ? z[i2] : v;
+                for (int i2 = 0; i2 < n; ++i2) v -= __bfloat162float(__float2bfloat16_rn(v));
+                return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            };
 #pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    qz[nt][j][c] = __shfl_sync(0xffffffffu, z[j], src) * a.scale_log2;
+            for (int u = 0; u < 2 * NZ; ++u) {
+                const int s0 = 8 * u + 2 * t, n = s0 / NG, j = s0 % NG;
+                qz[nt][u / 2][u % 2] = n < 3 ? term(n, j) | term(n, j + 1) << 16 : 0u;
+            }
+            // a power beyond FP32 belongs to scores beyond it
+            const float fac = a.scale_log2 * pow2((ex + 24) / 2) * pow2(ex + 24 - (ex + 24) / 2);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                f[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * c);  // of column 2t + c
                 const int cc = (qb * NT + nt) * 8 + 2 * t + c;
                 lim[nt][c] = cc < s.n * a.group ? s.len - s.n + 1 + cc / a.group : 0;
-                m[nt][c] = -FLT_MAX;
-                l[nt][c] = 0.f;
+                m[nt][c] = l[nt][c] = 0.f;
             }
 #pragma unroll
             for (int i2 = 0; i2 < MT; ++i2)
@@ -241,121 +277,121 @@ struct Warp {
         }
     }
 
-    // Adds the 16 tokens of one record; `full`: every column sees all of them.
-    __device__ __forceinline__ void block(const uint8_t* rec, int tok0, int len, bool full,
-                                          int lane) {
+    // Scores less the reference (log2 units) of the 16 tokens of one record.  FULL: every
+    // column sees all of them.
+    template <bool FULL>
+    __device__ __forceinline__ void scores(const uint8_t* rec, int tok0, int lane,
+                                           float (&sc)[NT][4]) {
         const int g = lane >> 2, t = lane & 3;
-        float sc[NT][4], zs[NT][4];
+        uint32_t k0[NG], k1[NG], s0[NG], s1[NG];
+        if constexpr (D == 256) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < 2; ++u) {
+                uint32_t w[4];
+                lds_words(rec + kv4_k_word(D, g, t + 16 * u), w);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[nt][c] = zs[nt][c] = 0.f;
-        {
-            uint32_t k0[NG], k1[NG], s0[NG], s1[NG];
-            if constexpr (D == 256) {
+                for (int i = 0; i < 4; ++i) k0[(4 * u + i) % NG] = w[i];
+                lds_words(rec + kv4_k_word(D, g + 8, t + 16 * u), w);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t w[4];
-                    lds_words(rec + kv4_k_word(D, g, t + 16 * u), w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) k0[(4 * u + i) % NG] = w[i];
-                    lds_words(rec + kv4_k_word(D, g + 8, t + 16 * u), w);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) k1[(4 * u + i) % NG] = w[i];
-                }
-            } else {
-                lds_words(rec + kv4_k_word(D, g, t), k0);
-                lds_words(rec + kv4_k_word(D, g + 8, t), k1);
+                for (int i = 0; i < 4; ++i) k1[(4 * u + i) % NG] = w[i];
             }
-            lds_words(rec + kv4_k_scale(D, g, 0), s0);
-            lds_words(rec + kv4_k_scale(D, g + 8, 0), s1);
+        } else {
+            lds_words(rec + kv4_k_word(D, g, t), k0);
+            lds_words(rec + kv4_k_word(D, g + 8, t), k1);
+        }
+        lds_words(rec + kv4_k_scale(D, g, 0), s0);
+        lds_words(rec + kv4_k_scale(D, g + 8, 0), s1);
+        // minima of groups 2t, 2t + 1 of the product's steps
+        const int jz = D == 64 ? 0 : D == 128 ? 2 * (t & 1) : 2 * t;
+        uint32_t z0[2], z1[2];
+        lds_words(rec + kv4_k_scale(D, g, jz), z0);
+        lds_words(rec + kv4_k_scale(D, g + 8, jz), z1);
+        const uint32_t za = __byte_perm(z0[0], z0[1], 0x7632), zb = __byte_perm(z1[0], z1[1], 0x7632);
+        float zs[NT][4];
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const uint32_t h0 = k0[j] >> 8, h1 = k1[j] >> 8;
-                const uint32_t lo = 0x000f000fu, up = 0x00f000f0u;
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(d, k0[j] & lo, k1[j] & lo, k0[j] & up, k1[j] & up, qf[nt][j][0],
-                            qf[nt][j][1]);
-                    mma_f16(d, h0 & lo, h1 & lo, h0 & up, h1 & up, qf[nt][j][2], qf[nt][j][3]);
-                    sc[nt][0] = fmaf(bf16_lo(s0[j]), d[0], sc[nt][0]);
-                    sc[nt][1] = fmaf(bf16_lo(s0[j]), d[1], sc[nt][1]);
-                    sc[nt][2] = fmaf(bf16_lo(s1[j]), d[2], sc[nt][2]);
-                    sc[nt][3] = fmaf(bf16_lo(s1[j]), d[3], sc[nt][3]);
-                    zs[nt][0] = fmaf(bf16_hi(s0[j]), qz[nt][j][0], zs[nt][0]);
-                    zs[nt][1] = fmaf(bf16_hi(s0[j]), qz[nt][j][1], zs[nt][1]);
-                    zs[nt][2] = fmaf(bf16_hi(s1[j]), qz[nt][j][0], zs[nt][2]);
-                    zs[nt][3] = fmaf(bf16_hi(s1[j]), qz[nt][j][1], zs[nt][3]);
-                }
+            for (int c = 0; c < 4; ++c) {
+                sc[nt][c] = 0.f;
+                zs[nt][c] = -m[nt][c & 1];
+            }
+            mma_bf16(zs[nt], za, zb, za, zb, qz[nt][0][0], qz[nt][0][1]);
+            if constexpr (NZ == 2) mma_bf16(zs[nt], za, zb, za, zb, qz[nt][1][0], qz[nt][1][1]);
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const uint32_t h0 = k0[j] >> 8, h1 = k1[j] >> 8;
+            const uint32_t lo = 0x000f000fu, up = 0x00f000f0u;
+            const float a0 = bf16_lo(s0[j]), a1 = bf16_lo(s1[j]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(d, k0[j] & lo, k1[j] & lo, k0[j] & up, k1[j] & up, qf[nt][j][0], qf[nt][j][1]);
+                mma_f16(d, h0 & lo, h1 & lo, h0 & up, h1 & up, qf[nt][j][2], qf[nt][j][3]);
+                sc[nt][0] = fmaf(a0, d[0], sc[nt][0]);
+                sc[nt][1] = fmaf(a0, d[1], sc[nt][1]);
+                sc[nt][2] = fmaf(a1, d[2], sc[nt][2]);
+                sc[nt][3] = fmaf(a1, d[3], sc[nt][3]);
             }
         }
-        bool up = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                float v = fmaf(sc[nt][c], f[nt][c & 1], zs[nt][c]);
-                if (!full && tok0 + g + 8 * (c >> 1) >= lim[nt][c & 1])
-                    v = -__int_as_float(0x7f800000);
-                sc[nt][c] = v;
-                up |= v > m[nt][c & 1] + 8.f;
+                sc[nt][c] = fmaf(sc[nt][c], f[nt][c & 1], zs[nt][c]);
+                if (!FULL && tok0 + g + 8 * (c >> 1) >= lim[nt][c & 1])
+                    sc[nt][c] = -__int_as_float(0x7f800000);
             }
-        if (__any_sync(0xffffffffu, up)) {  // move the maxima, rescale the sums
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v = fmaxf(sc[nt][c], sc[nt][c + 2]);
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    v = fmaxf(v, m[nt][c]);
-                    const float r = ex2(m[nt][c] - v);
-                    m[nt][c] = v;
-                    l[nt][c] *= r;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        o[nt][i][c] *= r;
-                        o[nt][i][c + 2] *= r;
-                    }
-                }
-        }
+    }
+
+    // Scales (x) and minima (y) of V of tokens r, r + 1 in the lane's group.
+    __device__ __forceinline__ uint2 scale_words(const uint8_t* rec, int r, int lane) {
+        return *reinterpret_cast<const uint2*>(rec + kv4_v_scale(D, r, (lane >> 2) / (256 / D)));
+    }
+    // The largest of what has to fit: s 2^9 and |z| 2^-14, as FP32 (NaN left out).
+    __device__ __forceinline__ float need(uint2 v) {
+        return fmaxf(fmaxf(bf16_lo(v.x), bf16_hi(v.x)) * 512.f,
+                     fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y))) * 6.103515625e-5f);
+    }
+    // FULL false: tokens at `len` and behind are left out; so is what is not finite, since it
+    // must not reach the columns that do not see its token.
+    template <bool FULL>
+    __device__ __forceinline__ void keep(uint2& v, int tok, int len, bool& odd) {
+        if (FULL) return;
+        const uint32_t in = (tok < len ? 0xffffu : 0u) | (tok + 1 < len ? 0xffff0000u : 0u);
+        v.x &= in;
+        v.y &= in;
+        uint32_t drop = 0u;
+        if ((v.x & 0x7f80u) == 0x7f80u || (v.y & 0x7f80u) == 0x7f80u) drop |= 0xffffu;
+        if ((v.x & 0x7f800000u) == 0x7f800000u || (v.y & 0x7f800000u) == 0x7f800000u)
+            drop |= 0xffff0000u;
+        odd |= drop != 0u;
+        v.x &= ~drop;
+        v.y &= ~drop;
+    }
+
+    // o += V^T P^T for the 16 tokens of one record.
+    template <bool FULL>
+    __device__ __forceinline__ void values(const uint8_t* rec, int tok0, int len, int lane, uint2 va,
+                                           uint2 vb, bool odd, const float (&sc)[NT][4]) {
+        const int g = lane >> 2, t = lane & 3;
         uint32_t b0[NT], b1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float p[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) p[c] = ex2(sc[nt][c] - m[nt][c & 1]);
+            for (int c = 0; c < 4; ++c) p[c] = ex2(sc[nt][c]);
             l[nt][0] += p[0] + p[2];
             l[nt][1] += p[1] + p[3];
-            b0[nt] = transpose8x8(pack_bf16x2(p[0], p[1]));
-            b1[nt] = transpose8x8(pack_bf16x2(p[2], p[3]));
+            b0[nt] = transpose8x8(pack_f16x2(p[0], p[1]));
+            b1[nt] = transpose8x8(pack_f16x2(p[2], p[3]));
         }
-        // V of tokens 2t, 2t+1 (a) and 2t+8, 2t+9 (b), dims [g D/8, (g+1) D/8)
-        constexpr int J = 256 / D;  // lanes g per group
-        uint2 sa = *reinterpret_cast<const uint2*>(rec + kv4_v_scale(D, 2 * t, g / J));
-        uint2 sb = *reinterpret_cast<const uint2*>(rec + kv4_v_scale(D, 2 * t + 8, g / J));
-        bool odd = false;
-        if (!full) {
-            // tokens behind the last are not read; what a token that only some columns see
-            // holds must not reach the others if it is not finite
-            auto keep = [&](uint2& v, int r) {
-                const uint32_t k = (tok0 + r < len ? 0xffffu : 0u) |
-                                   (tok0 + r + 1 < len ? 0xffff0000u : 0u);
-                v.x &= k;
-                v.y &= k;
-                uint32_t drop = 0u;
-                if (((v.x & 0x7f80u) == 0x7f80u) || ((v.y & 0x7f80u) == 0x7f80u)) drop |= 0xffffu;
-                if (((v.x & 0x7f800000u) == 0x7f800000u) || ((v.y & 0x7f800000u) == 0x7f800000u))
-                    drop |= 0xffff0000u;
-                odd |= drop != 0u;
-                v.x &= ~drop;
-                v.y &= ~drop;
-            };
-            keep(sa, 2 * t);
-            keep(sb, 2 * t + 8);
-        }
+        const float ps = pow2(24 - k), pz = pow2(-k);
+        const uint32_t sa = pack_f16x2(bf16_lo(va.x) * ps, bf16_hi(va.x) * ps);
+        const uint32_t sb = pack_f16x2(bf16_lo(vb.x) * ps, bf16_hi(vb.x) * ps);
+        const uint32_t za = pack_f16x2(bf16_lo(va.y) * pz, bf16_hi(va.y) * pz);
+        const uint32_t zb = pack_f16x2(bf16_lo(vb.y) * pz, bf16_hi(vb.y) * pz);
+        const uint32_t sa4 = hmul2(sa, 0x2c002c00u), sb4 = hmul2(sb, 0x2c002c00u);  // 2^-4
         uint32_t w0[VW], w1[VW], w8[VW], w9[VW];
         lds_words(rec + kv4_v_unit(D, 2 * t, g), w0);
         lds_words(rec + kv4_v_unit(D, 2 * t + 1, g), w1);
@@ -364,17 +400,20 @@ struct Warp {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const int w = i / 4, half = i / 2 % 2;
-            const uint32_t pa = __byte_perm(w0[w], w1[w], half ? 0x7632 : 0x5410);
-            const uint32_t pb = __byte_perm(w8[w], w9[w], half ? 0x7632 : 0x5410);
-            const int sh = 8 * (i & 1);
-            const uint32_t a0 = value2(pa >> sh, sa.x, sa.y);
-            const uint32_t a1 = value2(pa >> (sh + 4), sa.x, sa.y);
-            const uint32_t a2 = value2(pb >> sh, sb.x, sb.y);
-            const uint32_t a3 = value2(pb >> (sh + 4), sb.x, sb.y);
+            uint32_t pa = __byte_perm(w0[w], w1[w], half ? 0x7632 : 0x5410);
+            uint32_t pb = __byte_perm(w8[w], w9[w], half ? 0x7632 : 0x5410);
+            if (i & 1) {
+                pa >>= 8;
+                pb >>= 8;
+            }
+            const uint32_t a0 = hfma2(pa & 0x000f000fu, sa, za);
+            const uint32_t a1 = hfma2(pa & 0x00f000f0u, sa4, za);
+            const uint32_t a2 = hfma2(pb & 0x000f000fu, sb, zb);
+            const uint32_t a3 = hfma2(pb & 0x00f000f0u, sb4, zb);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(o[nt][i], a0, a1, a2, a3, b0[nt], b1[nt]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][i], a0, a1, a2, a3, b0[nt], b1[nt]);
         }
-        if (__any_sync(0xffffffffu, odd)) not_finite(rec, tok0, len, g);
+        if (!FULL && __any_sync(0xffffffffu, odd)) not_finite(rec, tok0, len, g);
     }
 
     // The columns that see a token whose V is not finite become NaN in that group's dims.
@@ -394,6 +433,72 @@ struct Warp {
                             o[nt][i][c + 2] = __int_as_float(0x7fffffff);
                         }
         }
+    }
+
+    // Adds the 32 tokens of one unit; `have`: bit i is set where record i is there.
+    template <bool FULL>
+    __device__ __forceinline__ void unit(const uint8_t* rec, int tok0, int len, int have, int lane) {
+        const uint8_t* rec1 = rec + 20 * D;
+        const int t = lane & 3;
+        // a record that is not there: no token of it is seen
+        const int t0 = FULL || (have & 1) ? tok0 : 0x40000000;
+        const int t1 = FULL || (have & 2) ? tok0 + kKv4Block : 0x40000000;
+        float sc0[NT][4], sc1[NT][4];
+        scores<FULL>(rec, t0, lane, sc0);
+        scores<FULL>(rec1, t1, lane, sc1);
+        uint2 v[4] = {scale_words(rec, 2 * t, lane), scale_words(rec, 2 * t + 8, lane),
+                      scale_words(rec1, 2 * t, lane), scale_words(rec1, 2 * t + 8, lane)};
+        bool odd0 = false, odd1 = false;
+        keep<FULL>(v[0], t0 + 2 * t, len, odd0);
+        keep<FULL>(v[1], t0 + 2 * t + 8, len, odd0);
+        keep<FULL>(v[2], t1 + 2 * t, len, odd1);
+        keep<FULL>(v[3], t1 + 2 * t + 8, len, odd1);
+        const float nd = fmaxf(fmaxf(need(v[0]), need(v[1])), fmaxf(need(v[2]), need(v[3])));
+        bool up = first || nd >= pow2(k);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                up |= fmaxf(fmaxf(sc0[nt][c], sc0[nt][c + 2]), fmaxf(sc1[nt][c], sc1[nt][c + 2])) > 8.f;
+        if (__any_sync(0xffffffffu, up)) raise(nd, sc0, sc1);
+        values<FULL>(rec, t0, len, lane, v[0], v[1], odd0, sc0);
+        values<FULL>(rec1, t1, len, lane, v[2], v[3], odd1, sc1);
+    }
+
+    // Moves the references to the unit's largest scores where they are above them (at the first
+    // unit in any case), and 2^k above what V needs; rescales the sums.
+    __device__ __forceinline__ void raise(float nd, float (&sc0)[NT][4], float (&sc1)[NT][4]) {
+        int kn = nd >= pow2(k) && k < 127 ? min(exponent(nd) + 1, 127) : k;
+        if (kn < k) kn = k;  // what is not finite asks for nothing
+#pragma unroll
+        for (int o2 = 1; o2 < (D == 64 ? 16 : D == 128 ? 8 : 4); o2 <<= 1)
+            kn = max(kn, __shfl_xor_sync(0xffffffffu, kn, o2));
+        const float rk = pow2(k - kn);
+        k = kn;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float v = fmaxf(fmaxf(sc0[nt][c], sc0[nt][c + 2]), fmaxf(sc1[nt][c], sc1[nt][c + 2]));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                if (first ? v == -__int_as_float(0x7f800000) : !(v > 0.f)) v = 0.f;
+                const float r = first ? 0.f : ex2(-v);
+                m[nt][c] += v;
+                l[nt][c] *= r;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    sc0[nt][c + 2 * i] -= v;
+                    sc1[nt][c + 2 * i] -= v;
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[nt][i][c] *= r * rk;
+                    o[nt][i][c + 2] *= r * rk;
+                }
+            }
+        first = false;
     }
 };
 
@@ -417,7 +522,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
     auto units_of = [&](int b, bool report) -> int64_t {
         if (b >= a.seqs) return 0;
         const Seq s = seq_of<QC>(a, b, report);
-        return (int64_t)s.blocks * s.qblocks * a.kv_heads;
+        return (int64_t)s.units * s.qblocks * a.kv_heads;
     };
     int64_t sum = 0;
     for (int b = threadIdx.x; b < a.seqs; b += kWarps * 32) sum += units_of(b, blockIdx.x == 0);
@@ -458,27 +563,28 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
     int b = sm.found_seq;
     int64_t seq_first = sm.found;
     Seq s = seq_of<QC>(a, b, false);
-    uint32_t phase = 0u, pending = 0u;  // per stage: parity waited for next, copy in flight
+    uint32_t phase = 0u, have = 0u;  // per stage: parity waited for next; records in flight
     bool dead = false;
     Warp<D, NT> st;
 
     for (int64_t u = begin; u < end;) {
-        while (u >= seq_first + (int64_t)s.blocks * s.qblocks * a.kv_heads) {
-            seq_first += (int64_t)s.blocks * s.qblocks * a.kv_heads;
+        while (u >= seq_first + (int64_t)s.units * s.qblocks * a.kv_heads) {
+            seq_first += (int64_t)s.units * s.qblocks * a.kv_heads;
             s = seq_of<QC>(a, ++b, false);  // u < total, so a sequence with work follows
         }
-        const int item = (int)((u - seq_first) / s.blocks);
-        const int64_t item_first = seq_first + (int64_t)item * s.blocks;
+        const int item = (int)((u - seq_first) / s.units);
+        const int64_t item_first = seq_first + (int64_t)item * s.units;
         const int k0 = (int)(u - item_first);
-        const int k1 = (int)min((int64_t)s.blocks, end - item_first);
+        const int k1 = (int)min((int64_t)s.units, end - item_first);
         const int qb = item / a.kv_heads, h = item - qb * a.kv_heads;
-        // every column sees the tokens before this
+        // every column sees the tokens before this one
         const int safe = s.len - s.n + 1 + qb * QC / a.group;
 
-        // record of this warp's x-th block (lane by lane); -1: page outside the cache
+        // record x & 1 of this warp's unit x / 2; -1: behind the end, or page outside the cache
+        const int records = (s.len + kKv4Block - 1) / kKv4Block;
         auto record = [&](int x) -> int {
-            const int kb = k0 + warp + x * kWarps;
-            if (kb >= k1) return -1;
+            const int ku = k0 + warp + (x >> 1) * kWarps, kb = 2 * ku + (x & 1);
+            if (ku >= k1 || kb >= records) return -1;
             const int p = kb / a.nb;
             const int page = __ldg(a.table + b * a.table_stride + p);
             if (page < 0 || page >= a.pages) {
@@ -487,23 +593,34 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
             }
             return (page * a.kv_heads + h) * a.nb + (kb - p * a.nb);
         };
-        auto issue = [&](int stage, int rec) {
-            if (rec < 0) return;
-            pending |= 1u << stage;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&sm.full[warp][stage], kRec);
-                bulk_load(sm.ring[warp][stage], a.cache + (int64_t)rec * kRec, kRec,
-                          &sm.full[warp][stage]);
+        // copies unit x's records (rec of this lane's window) to a stage; which ones there are
+        auto issue = [&](int stage, int window, int x) {
+            const int r0 = __shfl_sync(0xffffffffu, window, 2 * x & 31);
+            const int r1 = __shfl_sync(0xffffffffu, window, (2 * x + 1) & 31);
+            const uint32_t got = (r0 >= 0 ? 1u : 0u) | (r1 >= 0 ? 2u : 0u);
+            have = (have & ~(3u << (2 * stage))) | got << (2 * stage);
+            if (lane == 0 && got) {
+                uint64_t* bar = &sm.full[warp][stage];
+                uint8_t* dst = sm.ring[warp][stage];
+                mbar_arrive_expect_tx(bar, got == 3u ? 2 * kRec : kRec);
+                if (got == 3u && r1 == r0 + 1) {
+                    bulk_load(dst, a.cache + (int64_t)r0 * kRec, 2 * kRec, bar);
+                } else {
+                    if (r0 >= 0) bulk_load(dst, a.cache + (int64_t)r0 * kRec, kRec, bar);
+                    if (r1 >= 0) bulk_load(dst + kRec, a.cache + (int64_t)r1 * kRec, kRec, bar);
+                }
             }
         };
         const int n = dead ? 0 : max(0, (k1 - k0 - warp + kWarps - 1) / kWarps);
         int now = record(lane), next = record(32 + lane);
-        for (int i = 0; i < S && i < n; ++i) issue(i, __shfl_sync(0xffffffffu, now, i));
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (i < n) issue(i, now, i);
         st.begin(a, s, qb, h, lane);
         int stage = 0;
         for (int i = 0; i < n; ++i) {
-            const int rec = __shfl_sync(0xffffffffu, now, i & 31);
-            if (rec >= 0) {
+            const int got = (have >> (2 * stage)) & 3u;
+            if (got) {
                 const bool landed = mbar_wait(&sm.full[warp][stage], (phase >> stage) & 1u,
                                               a.limit_ns);
                 if (!__all_sync(0xffffffffu, landed)) {
@@ -512,24 +629,26 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
                     break;
                 }
                 phase ^= 1u << stage;
-                pending &= ~(1u << stage);
-                const int tok0 = (k0 + warp + i * kWarps) * kKv4Block;
-                st.block(sm.ring[warp][stage], tok0, s.len, tok0 + kKv4Block <= safe, lane);
+                have &= ~(3u << (2 * stage));
+                const int tok0 = (k0 + warp + i * kWarps) * kUnit;
+                if (got == 3 && tok0 + kUnit <= safe)
+                    st.template unit<true>(sm.ring[warp][stage], tok0, s.len, got, lane);
+                else
+                    st.template unit<false>(sm.ring[warp][stage], tok0, s.len, got, lane);
                 __syncwarp();
             }
             const int ahead = i + S;
-            const int rn = __shfl_sync(0xffffffffu, (ahead >> 5) == (i >> 5) ? now : next,
-                                       ahead & 31);
-            if (ahead < n) issue(stage, rn);
-            if ((i & 31) == 31) {
+            if (ahead < n) issue(stage, (ahead >> 4) == (i >> 4) ? now : next, ahead);
+            if ((i & 15) == 15) {
                 now = next;
-                next = record(i + 33 + lane);
+                next = record(2 * (i + 17) + lane);
             }
             stage = stage + 1 == S ? 0 : stage + 1;
         }
 
         // merge the warps
         const int g = lane >> 2, t = lane & 3;
+        const float pk = pow2(st.k);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -540,17 +659,17 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int col = nt * 8 + 2 * t + c;
                 if (g == 0) {
-                    sm.m[warp][col] = st.m[nt][c];
+                    sm.m[warp][col] = l == 0.f ? -FLT_MAX : st.m[nt][c];
                     sm.l[warp][col] = l;
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
                     *reinterpret_cast<float2*>(&sm.o[warp][col][g * (D / 8) + 2 * i]) =
-                        make_float2(st.o[nt][i][c], st.o[nt][i][c + 2]);
+                        make_float2(st.o[nt][i][c] * pk, st.o[nt][i][c + 2] * pk);
             }
         }
         __syncthreads();
-        const bool whole = k0 == 0 && k1 == s.blocks;
+        const bool whole = k0 == 0 && k1 == s.units;
         const int slot = item_first <= begin ? 0 : 1;
         for (int x = threadIdx.x; x < QC * D / 4; x += kWarps * 32) {
             const int col = x / (D / 4), d = x % (D / 4) * 4;
@@ -593,17 +712,19 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
     }
     // after a wait that ran out: the copies still in flight must land before the CTA ends
     for (int i = 0; i < S; ++i)
-        if ((pending >> i) & 1u)
+        if ((have >> (2 * i)) & 3u)
             if (!mbar_wait(&sm.full[warp][i], (phase >> i) & 1u, a.limit_ns) && lane == 0)
                 atomicOr(a.err, ERR_WAIT_DRAIN);
 }
 
 // Rows (query token blockIdx.x, head blockIdx.y) whose item lies in several CTAs, or has no
-// tokens at all.  D/4 lanes hold the row; the 512/D groups of lanes take the CTAs' partial sums
-// in turn and are merged in order.
+// tokens at all.  D/4 lanes hold the row; the 1024/D groups of lanes take the CTAs' partial sums
+// in turn, four loads at a time, and are merged in order.
+constexpr int kCombineThreads = 256;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(128) kv4_combine_kernel(const Args a, int ctas) {
-    constexpr int QC = 8 * NT, LN = D / 4, GR = 128 / LN;
+__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args a, int ctas) {
+    constexpr int QC = 8 * NT, LN = D / 4, GR = kCombineThreads / LN, U = 4;
     __shared__ float4 so[GR][LN];
     __shared__ float smx[GR], sl[GR];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -625,31 +746,43 @@ __global__ void __launch_bounds__(128) kv4_combine_kernel(const Args a, int ctas
     const int qb = idx / QC, col = idx - qb * QC;
     const int ln = threadIdx.x % LN, gr = threadIdx.x / LN;
     bf16* out = a.out + (int64_t)row * a.out_st + (int64_t)hq * a.out_sh + 4 * ln;
-    if (s.blocks == 0) {
+    if (s.units == 0) {
         if (gr == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
         if (threadIdx.x == 0 && a.lse)
             a.lse[(int64_t)row * a.heads + hq] = -__int_as_float(0x7f800000);
         return;
     }
     const int64_t per = share_of(a.prefix[a.seqs], ctas);
-    const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * s.blocks;
-    const int c0 = (int)(u0 / per), c1 = (int)((u0 + s.blocks - 1) / per);
+    const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * s.units;
+    const int c0 = (int)(u0 / per), c1 = (int)((u0 + s.units - 1) / per);
     if (c0 == c1) return;
     float m = -FLT_MAX, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + gr; c <= c1; c += GR) {
-        const int slot = u0 <= c * per ? 0 : 1;
-        const int64_t at = ((int64_t)c * 2 + slot) * QC + col;
-        const float2 ml = __ldcg(a.part_ml + at);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + ln);
-        const float mn = fmaxf(m, ml.x);
-        const float e0 = ex2(m - mn), e1 = ex2(ml.x - mn);
-        m = mn;
-        l = fmaf(e1, ml.y, e0 * l);
-        v.x = fmaf(e1, o.x, e0 * v.x);
-        v.y = fmaf(e1, o.y, e0 * v.y);
-        v.z = fmaf(e1, o.z, e0 * v.z);
-        v.w = fmaf(e1, o.w, e0 * v.w);
+    for (int c = c0 + gr; c <= c1; c += U * GR) {
+        float2 ml[U];
+        float4 o[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t cta = c + i * GR;
+            ml[i] = make_float2(-FLT_MAX, 0.f);
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cta <= c1) {
+                const int64_t at = (cta * 2 + (u0 <= cta * per ? 0 : 1)) * QC + col;
+                ml[i] = __ldcg(a.part_ml + at);
+                o[i] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + ln);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const float mn = fmaxf(m, ml[i].x);
+            const float e0 = ex2(m - mn), e1 = ex2(ml[i].x - mn);
+            m = mn;
+            l = fmaf(e1, ml[i].y, e0 * l);
+            v.x = fmaf(e1, o[i].x, e0 * v.x);
+            v.y = fmaf(e1, o[i].y, e0 * v.y);
+            v.z = fmaf(e1, o[i].z, e0 * v.z);
+            v.w = fmaf(e1, o[i].w, e0 * v.w);
+        }
     }
     so[gr][ln] = v;
     if (ln == 0) {
@@ -730,7 +863,7 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.tokens, (unsigned)c.heads);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
