@@ -49,8 +49,12 @@ constexpr int kCtasPerSm = 4;      // at most (sizes the workspace)
 constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
 constexpr int kMinShare = kWarps;  // least units per CTA: one for each warp
 
-// Ring stages of one unit per warp: about 64 KiB in flight per SM.
-__host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+// Ring stages of one unit per warp (two are 160 KiB in flight per SM at D = 128 and 256), and
+// the CTAs per SM that the registers are divided among.
+__host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : 2; }
+__host__ __device__ constexpr int ctas_of(int D, int NT) {
+    return D == 256 || NT == 4 || (D == 128 && NT == 2) ? 2 : NT == 2 ? 3 : 4;
+}
 
 struct Args {
     const bf16* q;
@@ -69,7 +73,12 @@ struct Args {
     uint64_t limit_ns;
     int64_t pages;
     int tokens, seqs, heads, kv_heads, group, table_width, nb;
+    uint64_t group_inv;  // 2^64 / group, rounded up
     float scale_log2;
+    // n / group, 0 <= n < 2^31 (exact: the inverse is off by less than group / 2^64)
+    __device__ __forceinline__ int over_group(int n) const {
+        return group == 1 ? n : (int)__umul64hi((uint64_t)n, group_inv);
+    }
 };
 
 // One sequence's share of the problem.
@@ -97,7 +106,8 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool report) {
 }
 
 __device__ __forceinline__ int64_t share_of(int64_t units, int ctas) {
-    const int64_t per = (units + ctas - 1) / ctas;
+    const int64_t up = units + ctas - 1;
+    const int64_t per = up >> 32 ? up / ctas : (int64_t)((uint32_t)up / (uint32_t)ctas);
     return per < kMinShare ? kMinShare : per;
 }
 
@@ -176,18 +186,30 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 }
 
 
+// Shared memory of a CTA.  A warp's sums at the end of an item take the place of its own ring,
+// which is empty then; dims are in the order of the fragments (dim_of), which keeps the stores
+// free of bank conflicts.
 template <int D, int NT>
 struct Smem {
     static constexpr int S = stages_of(D);
     static constexpr int QC = 8 * NT;
-    static constexpr int OS = D + 4;  // padded row of the merge buffer
-    uint8_t ring[kWarps][S][2 * 20 * D];
-    float o[kWarps][QC][OS];
+    static constexpr int OS = D + 4;  // padded row of the sums
+    union PerWarp {
+        uint8_t ring[S][2 * 20 * D];
+        float o[QC][OS];
+    } w[kWarps];
     float m[kWarps][QC], l[kWarps][QC];
     uint64_t full[kWarps][S];
     int64_t sum[kWarps], found;
     int found_seq;
 };
+
+// First of the two dims in the n-th pair of a row of sums: pairs run over g, then over the
+// dims of a lane.
+template <int D>
+__device__ __forceinline__ int dim_of(int n) {
+    return (n & 7) * (D / 8) + 2 * (n >> 3);
+}
 
 // The columns' state of one warp over one item.
 template <int D, int NT>
@@ -216,7 +238,7 @@ struct Warp {
             float x[NG][8];
             float amax = 0.f;
             const bool ok = col < s.n * a.group;
-            const int i = ok ? col / a.group : 0;
+            const int i = ok ? a.over_group(col) : 0;
             const bf16* row = a.q + (int64_t)(s.q0 + i) * a.q_st +
                               (int64_t)(h * a.group + (ok ? col - i * a.group : 0)) * a.q_sh;
 #pragma unroll
@@ -248,18 +270,32 @@ struct Warp {
                     qf[nt][j][e] = pack_f16x2(x[j][e] * p1 * p2 * d, x[j][e + 4] * p1 * p2 * d);
                 }
             }
-            // z = z0 + z1 + z2 in bf16; step (term, group) of the minima's product
-            auto term = [&](int n, int j) -> uint32_t {
-                float v = 0.f;
+            // the lane's two groups of the minima's product, each sum as three bf16 terms
+            float u0 = z[0], u1 = z[1];
 #pragma unroll
-                for (int i2 = 0; i2 < NG; ++i2) v = i2 == j ? z[i2] : v;
-                for (int i2 = 0; i2 < n; ++i2) v -= __bfloat162float(__float2bfloat16_rn(v));
-                return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-            };
+            for (int j = 2; j < NG; j += 2) {
+                const bool mine = j == ((NG - 1) & (2 * t));
+                u0 = mine ? z[j] : u0;
+                u1 = mine ? z[j + 1] : u1;
+            }
+            uint32_t term[3];
 #pragma unroll
-            for (int u = 0; u < 2 * NZ; ++u) {
-                const int s0 = 8 * u + 2 * t, n = s0 / NG, j = s0 % NG;
-                qz[nt][u / 2][u % 2] = n < 3 ? term(n, j) | term(n, j + 1) << 16 : 0u;
+            for (int e = 0; e < 3; ++e) {
+                term[e] = pack_bf16x2(u0, u1);
+                u0 -= bf16_lo(term[e]);
+                u1 -= bf16_hi(term[e]);
+            }
+            if constexpr (D == 64) {  // steps: terms 0, 1, 2, none by t
+                qz[nt][0][0] = t == 0 ? term[0] : t == 1 ? term[1] : t == 2 ? term[2] : 0u;
+                qz[nt][0][1] = 0u;
+            } else if constexpr (D == 128) {  // term 0 | 1 by t / 2, then 2 | none
+                qz[nt][0][0] = t < 2 ? term[0] : term[1];
+                qz[nt][0][1] = t < 2 ? term[2] : 0u;
+            } else {
+                qz[nt][0][0] = term[0];
+                qz[nt][0][1] = term[1];
+                qz[nt][NZ - 1][0] = term[2];
+                qz[nt][NZ - 1][1] = 0u;
             }
             // a power beyond FP32 belongs to scores beyond it
             const float fac = a.scale_log2 * pow2((ex + 24) / 2) * pow2(ex + 24 - (ex + 24) / 2);
@@ -267,7 +303,7 @@ struct Warp {
             for (int c = 0; c < 2; ++c) {
                 f[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * c);  // of column 2t + c
                 const int cc = (qb * NT + nt) * 8 + 2 * t + c;
-                lim[nt][c] = cc < s.n * a.group ? s.len - s.n + 1 + cc / a.group : 0;
+                lim[nt][c] = cc < s.n * a.group ? s.len - s.n + 1 + a.over_group(cc) : 0;
                 m[nt][c] = l[nt][c] = 0.f;
             }
 #pragma unroll
@@ -503,7 +539,7 @@ struct Warp {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a) {
+__global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_kernel(const Args a) {
     using Sm = Smem<D, NT>;
     constexpr int S = Sm::S, QC = Sm::QC;
     constexpr uint32_t kRec = 20 * D;
@@ -572,13 +608,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
             seq_first += (int64_t)s.units * s.qblocks * a.kv_heads;
             s = seq_of<QC>(a, ++b, false);  // u < total, so a sequence with work follows
         }
-        const int item = (int)((u - seq_first) / s.units);
+        const int64_t in_seq = u - seq_first;
+        const int item = in_seq >> 32 ? (int)(in_seq / s.units) : (int)((uint32_t)in_seq / (uint32_t)s.units);
         const int64_t item_first = seq_first + (int64_t)item * s.units;
         const int k0 = (int)(u - item_first);
         const int k1 = (int)min((int64_t)s.units, end - item_first);
         const int qb = item / a.kv_heads, h = item - qb * a.kv_heads;
         // every column sees the tokens before this one
-        const int safe = s.len - s.n + 1 + qb * QC / a.group;
+        const int safe = s.len - s.n + 1 + a.over_group(qb * QC);
 
         // record x & 1 of this warp's unit x / 2; -1: behind the end, or page outside the cache
         const int records = (s.len + kKv4Block - 1) / kKv4Block;
@@ -601,7 +638,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
             have = (have & ~(3u << (2 * stage))) | got << (2 * stage);
             if (lane == 0 && got) {
                 uint64_t* bar = &sm.full[warp][stage];
-                uint8_t* dst = sm.ring[warp][stage];
+                uint8_t* dst = sm.w[warp].ring[stage];
                 mbar_arrive_expect_tx(bar, got == 3u ? 2 * kRec : kRec);
                 if (got == 3u && r1 == r0 + 1) {
                     bulk_load(dst, a.cache + (int64_t)r0 * kRec, 2 * kRec, bar);
@@ -632,9 +669,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
                 have &= ~(3u << (2 * stage));
                 const int tok0 = (k0 + warp + i * kWarps) * kUnit;
                 if (got == 3 && tok0 + kUnit <= safe)
-                    st.template unit<true>(sm.ring[warp][stage], tok0, s.len, got, lane);
+                    st.template unit<true>(sm.w[warp].ring[stage], tok0, s.len, got, lane);
                 else
-                    st.template unit<false>(sm.ring[warp][stage], tok0, s.len, got, lane);
+                    st.template unit<false>(sm.w[warp].ring[stage], tok0, s.len, got, lane);
                 __syncwarp();
             }
             const int ahead = i + S;
@@ -664,49 +701,47 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_kernel(const Args a
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    *reinterpret_cast<float2*>(&sm.o[warp][col][g * (D / 8) + 2 * i]) =
+                    *reinterpret_cast<float2*>(&sm.w[warp].o[col][16 * i + 2 * g]) =
                         make_float2(st.o[nt][i][c] * pk, st.o[nt][i][c + 2] * pk);
             }
         }
         __syncthreads();
         const bool whole = k0 == 0 && k1 == s.units;
         const int slot = item_first <= begin ? 0 : 1;
-        for (int x = threadIdx.x; x < QC * D / 4; x += kWarps * 32) {
-            const int col = x / (D / 4), d = x % (D / 4) * 4;
+        for (int x = threadIdx.x; x < QC * D / 2; x += kWarps * 32) {
+            const int col = x / (D / 2), n = x % (D / 2);
             const int idx = qb * QC + col;
             if (idx >= s.n * a.group) continue;
             float m = sm.m[0][col];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm.m[w][col]);
             float l = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float e = ex2(sm.m[w][col] - m);
-                const float4 o = *reinterpret_cast<const float4*>(&sm.o[w][col][d]);
+                const float2 o = *reinterpret_cast<const float2*>(&sm.w[w].o[col][2 * n]);
                 l = fmaf(e, sm.l[w][col], l);
                 v.x = fmaf(e, o.x, v.x);
                 v.y = fmaf(e, o.y, v.y);
-                v.z = fmaf(e, o.z, v.z);
-                v.w = fmaf(e, o.w, v.w);
             }
             if (whole) {
                 const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-                const int i = idx / a.group, hq = h * a.group + idx - i * a.group;
-                const uint2 r = make_uint2(pack_bf16x2(v.x * inv, v.y * inv),
-                                           pack_bf16x2(v.z * inv, v.w * inv));
-                *reinterpret_cast<uint2*>(a.out + (int64_t)(s.q0 + i) * a.out_st +
-                                          (int64_t)hq * a.out_sh + d) = r;
-                if (d == 0 && a.lse)
+                const int i = a.over_group(idx), hq = h * a.group + idx - i * a.group;
+                *reinterpret_cast<uint32_t*>(a.out + (int64_t)(s.q0 + i) * a.out_st +
+                                             (int64_t)hq * a.out_sh + dim_of<D>(n)) =
+                    pack_bf16x2(v.x * inv, v.y * inv);
+                if (n == 0 && a.lse)
                     a.lse[(int64_t)(s.q0 + i) * a.heads + hq] =
                         l == 0.f ? -__int_as_float(0x7f800000)
                                  : (m + log2f(l)) * 0.693147180559945309f;
             } else {
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * QC + col;
-                *reinterpret_cast<float4*>(a.part + at * D + d) = v;
-                if (d == 0) a.part_ml[at] = make_float2(m, l);
+                *reinterpret_cast<float2*>(a.part + at * D + 2 * n) = v;
+                if (n == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is next
         __syncthreads();
         u = item_first + k1;
     }
@@ -745,9 +780,9 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
     const int idx = (row - s.q0) * a.group + hq - h * a.group;
     const int qb = idx / QC, col = idx - qb * QC;
     const int ln = threadIdx.x % LN, gr = threadIdx.x / LN;
-    bf16* out = a.out + (int64_t)row * a.out_st + (int64_t)hq * a.out_sh + 4 * ln;
+    bf16* out = a.out + (int64_t)row * a.out_st + (int64_t)hq * a.out_sh;
     if (s.units == 0) {
-        if (gr == 0) *reinterpret_cast<uint2*>(out) = make_uint2(0u, 0u);
+        if (gr == 0) *reinterpret_cast<uint2*>(out + 4 * ln) = make_uint2(0u, 0u);
         if (threadIdx.x == 0 && a.lse)
             a.lse[(int64_t)row * a.heads + hq] = -__int_as_float(0x7f800000);
         return;
@@ -806,8 +841,8 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
         v.w = fmaf(e, o.w, v.w);
     }
     const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln)) = pack_bf16x2(v.x * inv, v.y * inv);
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln + 1)) = pack_bf16x2(v.z * inv, v.w * inv);
     if (ln == 0 && a.lse)
         a.lse[(int64_t)row * a.heads + hq] = l == 0.f ? -__int_as_float(0x7f800000)
                                                        : (m + log2f(l)) * 0.693147180559945309f;
@@ -841,6 +876,7 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     a.heads = c.heads;
     a.kv_heads = c.kv_heads;
     a.group = c.heads / c.kv_heads;
+    a.group_inv = a.group == 1 ? 0 : ~0ull / (uint64_t)a.group + 1;
     a.table_width = c.table_width;
     a.nb = c.blocks_per_page;
     a.scale_log2 = c.scale * 1.44269504088896340736f;
