@@ -129,13 +129,69 @@ struct BwdArgs {
     float eps;
 };
 
+// 16 bytes from global to this lane's own place in shared memory; `bytes` 0 writes zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Shared memory of the backward: every lane's ring of its own 16-byte pieces (x and g of one
+// chunk per stage), and its (high, low) sums.
+template <typename T>
+struct BwdSmem {
+    static constexpr int V = sizeof(T) / 2;  // pieces per vector of 8 elements
+    static constexpr int NV = 4 * V;         // pieces per stage: two vectors of x, two of g
+    static constexpr int S = sizeof(T) == 2 ? 5 : 3;  // 10 and 12 KiB per warp
+    union {
+        uint4 ring[kWarps][S][NV][32];
+        float merge[kWarps][2][256];
+    };
+    ulonglong2 sums[2][4][kWarps * 32];  // high, low: four pairs of f2 per lane
+};
+
+// Eight elements at a lane's place in the ring, as FP32 pairs.
+template <typename T>
+__device__ __forceinline__ void pairs8(const uint4* p, f2 (&f)[4]) {
+    if constexpr (sizeof(T) == 2) {
+        Pairs<__nv_bfloat16>::get(p[0], f);
+    } else {
+        const uint4 a = p[0], b = p[32];
+        f[0] = f2_make(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = f2_make(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = f2_make(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = f2_make(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const f2 (&f)[4]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = Pairs<__nv_bfloat16>::put(f);
+    } else {
+        reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
+        reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
+    }
+}
+
 // Persistent: the first grid[0] CTAs take q's units, the others k's; a unit is tpw tokens and
-// one part of their heads.  Every lane keeps the (high, low) TwoSum pair of its 16 columns of
-// dw over all its rows; the pairs of the CTA's lanes are merged in a fixed order and written
-// to the workspace, whose CTA partials qk_dw_reduce_kernel adds in a fixed order.
+// one part of their heads (up to 8 chunks).  Rows stream through a ring in shared memory that
+// belongs to the lane alone (asynchronous copies, no barriers), so the bytes in flight do not
+// cost registers.  A lane adds the dw terms of a unit's chunks in FP32, and each unit's sum to
+// a (high, low) pair with TwoSum; the pairs of the CTA's lanes are merged in a fixed order and
+// written to the workspace, whose CTA partials qk_dw_reduce_kernel adds in a fixed order.
+// Two-element FP32 instructions halve the arithmetic.  Measured on GB300 at T = 32768, 32 + 8
+// heads of 128, bf16: 373 us with register loads, scalar arithmetic and TwoSum per term.
 template <typename T, int LPR, bool NB>
-__global__ void __launch_bounds__(kWarps * 32) qk_bwd_kernel(const BwdArgs a) {
-    constexpr int RPW = 32 / LPR;
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
+    qk_bwd_kernel(const BwdArgs a) {
+    using Sm = BwdSmem<T>;
+    constexpr int RPW = 32 / LPR, S = Sm::S, V = Sm::V, NV = Sm::NV;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
     const int side = (int)blockIdx.x < a.grid[0] ? 0 : 1;
     const int cta = blockIdx.x - (side ? a.grid[0] : 0);
     const Span sp = a.span[side];
@@ -143,149 +199,222 @@ __global__ void __launch_bounds__(kWarps * 32) qk_bwd_kernel(const BwdArgs a) {
     const int lane = threadIdx.x & 31, l = lane % LPR, rr = lane / LPR;
     const int hsub = rr & ((1 << sp.log_hpw) - 1), tsub = rr >> sp.log_hpw;
     const int tpw = RPW >> sp.log_hpw;
-    const int64_t groups = ((int64_t)a.tokens + tpw - 1) / tpw;
-    const int64_t units = groups * sp.parts;
+    const int64_t units = ((int64_t)a.tokens + tpw - 1) / tpw * sp.parts;
+    const int64_t stride = (int64_t)a.grid[side] * kWarps;
     const bool dims_ok = 16 * l < a.D;
 
     RowLane<NB> rl;
     rl.init(l, a.rope.rd);
-    float w0[8], w1[8];
-    f2 hi[8], lo[8];
+    f2 w0[4], w1[4], acc[8];
+    {
+        float f0[8], f1[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        w0[i] = w1[i] = 0.f;
-        hi[i] = lo[i] = 0ull;
-    }
-    if (dims_ok) {
-        load_w8(a.w[side], a.w_bf16, rl.off0, w0);
-        load_w8(a.w[side], a.w_bf16, rl.off1, w1);
+        for (int i = 0; i < 8; ++i) f0[i] = f1[i] = 0.f;
+        if (dims_ok) {
+            load_w8(a.w[side], a.w_bf16, rl.off0, f0);
+            load_w8(a.w[side], a.w_bf16, rl.off1, f1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w0[i] = f2_make(f0[2 * i], f0[2 * i + 1]);
+            w1[i] = f2_make(f1[2 * i], f1[2 * i + 1]);
+            sm.sums[0][i][threadIdx.x] = sm.sums[1][i][threadIdx.x] = make_ulonglong2(0ull, 0ull);
+        }
     }
     const int64_t sxh = a.x[side].sh, sgh = a.g[side].sh, sdh = a.dx[side].sh;
     const float inv_d = __frcp_rn((float)a.D);
 
-    for (int64_t unit = (int64_t)cta * kWarps + warp; unit < units;
-         unit += (int64_t)a.grid[side] * kWarps) {
-        const int64_t grp = sp.parts == 1 ? unit : unit / sp.parts;
-        const int part = (int)(unit - grp * sp.parts);
-        const Token tk = find_token((int)min(grp * tpw + tsub, (int64_t)a.tokens), a.tokens, a.T,
-                                    a.rope, a.err, side == 0 && part == 0 && l == 0 && hsub == 0);
-        const bool ok = tk.ok && dims_ok;
-        const T* x = a.x[side].row<T>(tk.b, tk.t);
-        const T* g = a.g[side].row<T>(tk.b, tk.t);
-        T* dx = a.dx[side].row<T>(tk.b, tk.t);
-        const int c0 = part * sp.per_part, c1 = min(sp.chunks, c0 + sp.per_part);
-
-        auto fetch = [&](int c, Raw8<T>& x0, Raw8<T>& x1, Raw8<T>& g0, Raw8<T>& g1) {
-            const int h = (c << sp.log_hpw) + hsub;
-            if (ok && h < sp.heads) {
-                x0.load(x + h * sxh + rl.off0);
-                x1.load(x + h * sxh + rl.off1);
-                g0.load(g + h * sgh + rl.off0);
-                g1.load(g + h * sgh + rl.off1);
-            } else {
-                x0.clear();
-                x1.clear();
-                g0.clear();
-                g1.clear();
+    // A place in the warp's line of chunks.
+    struct At {
+        int64_t unit;
+        int c, c1, tok;
+    };
+    auto enter = [&](At& at) {  // the unit's part of the heads and this row's token
+        const int64_t grp = sp.parts == 1 ? at.unit
+                            : (at.unit >> 32) ? at.unit / sp.parts
+                                              : (int64_t)((uint32_t)at.unit / (uint32_t)sp.parts);
+        const int part = (int)(at.unit - grp * sp.parts);
+        at.c = part * sp.per_part;
+        at.c1 = min(sp.chunks, at.c + sp.per_part);
+        at.tok = (int)min(grp * tpw + tsub, (int64_t)a.tokens);
+    };
+    const uint32_t ring = smem_addr(&sm.ring[warp][0][0][lane]);
+    const T *px = nullptr, *pg = nullptr;  // the copying side's rows
+    At in{(int64_t)cta * kWarps + warp, 0, 0, 0};
+    auto rows_in = [&]() {
+        if (in.unit >= units) return;
+        enter(in);
+        const int t = in.tok < a.tokens ? in.tok : 0;
+        const int b = a.tokens == a.T ? 0 : t / a.T;
+        px = a.x[side].row<T>(b, t - b * a.T);
+        pg = a.g[side].row<T>(b, t - b * a.T);
+    };
+    auto fetch = [&](int stage) {  // the next chunk, if there is one
+        if (in.unit < units) {
+            const int h = (in.c << sp.log_hpw) + hsub;
+            const bool ok = in.tok < a.tokens && dims_ok && h < sp.heads;
+            const uint32_t n = ok ? 16u : 0u;
+            const int64_t hx = ok ? h * sxh : 0, hg = ok ? h * sgh : 0;
+            const uint32_t dst = ring + (uint32_t)stage * (NV * 512);
+            const int o0 = ok ? rl.off0 : 0, o1 = ok ? rl.off1 : 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                copy16(dst + i * 512, px + hx + o0 + 4 * i, n);
+                copy16(dst + (V + i) * 512, px + hx + o1 + 4 * i, n);
+                copy16(dst + (2 * V + i) * 512, pg + hg + o0 + 4 * i, n);
+                copy16(dst + (3 * V + i) * 512, pg + hg + o1 + 4 * i, n);
             }
-        };
-        Raw8<T> x0, x1, g0, g1;
-        fetch(c0, x0, x1, g0, g1);
+            if (++in.c == in.c1) {
+                in.unit += stride;
+                rows_in();
+            }
+        }
+        copy_commit();
+    };
+    rows_in();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch(i);
+
+    int stage = 0;
+    for (At at{(int64_t)cta * kWarps + warp, 0, 0, 0}; at.unit < units; at.unit += stride) {
+        enter(at);
+        const Token tk = find_token(at.tok, a.tokens, a.T, a.rope, a.err,
+                                    side == 0 && at.c == 0 && l == 0 && hsub == 0);
+        const bool ok = tk.ok && dims_ok;
+        T* dx = a.dx[side].row<T>(tk.b, tk.t);
         Angles ang;
         ang.identity();
         if (ok && rl.turns) {
-            const int64_t at = tk.pos * (a.rope.rd / 2) + 8 * l;
-            ang.load(a.rope.cos + at, a.rope.sin + at);
+            const int64_t p = tk.pos * (a.rope.rd / 2) + 8 * l;
+            ang.load(a.rope.cos + p, a.rope.sin + p);
         }
-        for (int c = c0; c < c1; ++c) {
-            Raw8<T> nx0, nx1, ng0, ng1;
-            if (c + 1 < c1) fetch(c + 1, nx0, nx1, ng0, ng1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+        for (int c = at.c; c < at.c1; ++c) {
             const int h = (c << sp.log_hpw) + hsub;
-            float xu[8], xv[8], hu[8], hv[8];
-            x0.get(xu);
-            x1.get(xv);
-            g0.get(hu);
-            g1.get(hv);
-            rotate<NB, true>(hu, hv, ang);
-            float ss = 0.f, dot = 0.f;
+            copy_wait<S - 2>();
+            const uint4* slot = &sm.ring[warp][stage][0][lane];
+            f2 x0[4], x1[4], h0[4], h1[4];
+            pairs8<T>(slot, x0);
+            pairs8<T>(slot + 32 * V, x1);
+            pairs8<T>(slot + 64 * V, h0);
+            pairs8<T>(slot + 96 * V, h1);
+            // the slot read one chunk ago is free: every lane reads its own
+            fetch(stage == 0 ? S - 1 : stage - 1);
+            stage = stage + 1 == S ? 0 : stage + 1;
+
+            if constexpr (NB) {
+                float u[8], v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(xu[e], xu[e], ss);
-                dot = fmaf(hu[e] * w0[e], xu[e], dot);
+                for (int i = 0; i < 4; ++i) {
+                    u[2 * i] = f2_lo(h0[i]);
+                    u[2 * i + 1] = f2_hi(h0[i]);
+                    v[2 * i] = f2_lo(h1[i]);
+                    v[2 * i + 1] = f2_hi(h1[i]);
+                }
+                rotate<true, true>(u, v, ang);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h0[i] = f2_make(u[2 * i], u[2 * i + 1]);
+                    h1[i] = f2_make(v[2 * i], v[2 * i + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f2 cc = f2_make(ang.c[2 * i], ang.c[2 * i + 1]);
+                    const f2 s2 = f2_make(ang.s[2 * i], ang.s[2 * i + 1]);
+                    const f2 n2 = f2_make(-ang.s[2 * i], -ang.s[2 * i + 1]);
+                    const f2 y = h0[i];
+                    h0[i] = fma2(h1[i], s2, mul2(y, cc));
+                    h1[i] = fma2(y, n2, mul2(h1[i], cc));
+                }
+            }
+            f2 ss2 = 0ull, dot2 = 0ull;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ss2 = fma2(x0[i], x0[i], ss2);
+                dot2 = fma2(mul2(h0[i], w0[i]), x0[i], dot2);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(xv[e], xv[e], ss);
-                dot = fmaf(hv[e] * w1[e], xv[e], dot);
+            for (int i = 0; i < 4; ++i) {
+                ss2 = fma2(x1[i], x1[i], ss2);
+                dot2 = fma2(mul2(h1[i], w1[i]), x1[i], dot2);
             }
-            ss = row_sum<LPR>(ss);
-            dot = row_sum<LPR>(dot);
+            const float ss = row_sum<LPR>(f2_lo(ss2) + f2_hi(ss2));
+            const float dot = row_sum<LPR>(f2_lo(dot2) + f2_hi(dot2));
             const float r = row_rstd(ss, (float)a.D, a.eps);
-            const float k = r * (r * (dot * inv_d));  // r^2 mean(g x)
-            const bool store = ok && h < sp.heads;
-            if (store) {
+            // dx = r (h w) - x r k,  k = r^2 mean(g x)
+            const f2 r2 = f2_splat(r), nk = f2_splat(-(r * (r * (r * (dot * inv_d)))));
+            if (ok && h < sp.heads) {
+                f2 d[4];
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    comp_add2(hi[e / 2], lo[e / 2],
-                              f2_make(hu[e] * (xu[e] * r), hu[e + 1] * (xu[e + 1] * r)));
-                    comp_add2(hi[4 + e / 2], lo[4 + e / 2],
-                              f2_make(hv[e] * (xv[e] * r), hv[e + 1] * (xv[e + 1] * r)));
+                for (int i = 0; i < 4; ++i) {
+                    acc[i] = fma2(h0[i], mul2(x0[i], r2), acc[i]);
+                    d[i] = fma2(x0[i], nk, mul2(mul2(h0[i], w0[i]), r2));
                 }
+                store8<T>(dx + h * sdh + rl.off0, d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    xu[e] = r * fmaf(-xu[e], k, hu[e] * w0[e]);
-                    xv[e] = r * fmaf(-xv[e], k, hv[e] * w1[e]);
+                for (int i = 0; i < 4; ++i) {
+                    acc[4 + i] = fma2(h1[i], mul2(x1[i], r2), acc[4 + i]);
+                    d[i] = fma2(x1[i], nk, mul2(mul2(h1[i], w1[i]), r2));
                 }
-                x0.set(xu);
-                x1.set(xv);
-                x0.store(dx + h * sdh + rl.off0);
-                x1.store(dx + h * sdh + rl.off1);
+                store8<T>(dx + h * sdh + rl.off1, d);
             }
-            x0 = nx0;
-            x1 = nx1;
-            g0 = ng0;
-            g1 = ng1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ulonglong2 hi = sm.sums[0][i][threadIdx.x], lo = sm.sums[1][i][threadIdx.x];
+            f2 h0 = hi.x, l0 = lo.x, h1 = hi.y, l1 = lo.y;
+            comp_add2(h0, l0, acc[2 * i]);
+            comp_add2(h1, l1, acc[2 * i + 1]);
+            sm.sums[0][i][threadIdx.x] = make_ulonglong2(h0, h1);
+            sm.sums[1][i][threadIdx.x] = make_ulonglong2(l0, l1);
         }
     }
+    copy_wait<0>();
+    __syncthreads();
 
     // merge the warp's rows (lanes of equal l), then the warps in order
-    __shared__ float sm[kWarps][2][256];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float h0 = f2_lo(hi[i]), h1 = f2_hi(hi[i]), e0 = f2_lo(lo[i]), e1 = f2_hi(lo[i]);
+        const ulonglong2 hi = sm.sums[0][i / 2][threadIdx.x], lo = sm.sums[1][i / 2][threadIdx.x];
+        const f2 hh = i & 1 ? hi.y : hi.x, ll = i & 1 ? lo.y : lo.x;
+        float h0 = f2_lo(hh), h1 = f2_hi(hh), e0 = f2_lo(ll), e1 = f2_hi(ll);
 #pragma unroll
         for (int o = LPR; o < 32; o <<= 1) {
-            comp_merge(h0, e0, __shfl_xor_sync(0xffffffffu, h0, o),
-                       __shfl_xor_sync(0xffffffffu, e0, o));
-            comp_merge(h1, e1, __shfl_xor_sync(0xffffffffu, h1, o),
-                       __shfl_xor_sync(0xffffffffu, e1, o));
+            const float a0 = __shfl_xor_sync(0xffffffffu, h0, o), b0 = __shfl_xor_sync(0xffffffffu, e0, o);
+            const float a1 = __shfl_xor_sync(0xffffffffu, h1, o), b1 = __shfl_xor_sync(0xffffffffu, e1, o);
+            comp_merge(h0, e0, a0, b0);
+            comp_merge(h1, e1, a1, b1);
         }
         if (rr == 0 && dims_ok) {
             const int col = (i < 4 ? rl.off0 : rl.off1 - 8) + 2 * i;
-            sm[warp][0][col] = h0;
-            sm[warp][0][col + 1] = h1;
-            sm[warp][1][col] = e0;
-            sm[warp][1][col + 1] = e1;
+            sm.merge[warp][0][col] = h0;
+            sm.merge[warp][0][col + 1] = h1;
+            sm.merge[warp][1][col] = e0;
+            sm.merge[warp][1][col + 1] = e1;
         }
     }
     __syncthreads();
     for (int col = threadIdx.x; col < a.D; col += kWarps * 32) {
-        float h = sm[0][0][col], e = sm[0][1][col];
+        float h = sm.merge[0][0][col], e = sm.merge[0][1][col];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) comp_merge(h, e, sm[i][0][col], sm[i][1][col]);
+        for (int i = 1; i < kWarps; ++i) comp_merge(h, e, sm.merge[i][0][col], sm.merge[i][1][col]);
         float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D + col;
         out[0] = h;
         out[a.D] = e;
     }
 }
 
-// dwq and dwk from the CTA partials: one CTA per 32 columns of one of them; warp s of 8 adds
-// the partials s, s + 8, ... in order, the eight sums are merged in order, and high + low is
+// dwq and dwk from the CTA partials: one CTA per 32 columns of one of them; warp w of 32 adds
+// the partials w, w + 32, ... in order, the 32 sums are merged by a fixed tree, and high + low is
 // rounded once.
-__global__ void __launch_bounds__(256) qk_dw_reduce_kernel(const float* __restrict__ ws,
-                                                           float* dwq, float* dwk, int D, int gq,
-                                                           int gk) {
-    __shared__ float sh[8][32], sl[8][32];
+constexpr int kReduceWarps = 32;
+
+__global__ void __launch_bounds__(kReduceWarps * 32)
+    qk_dw_reduce_kernel(const float* __restrict__ ws, float* dwq, float* dwk, int D, int gq, int gk) {
+    __shared__ float sh[kReduceWarps][33], sl[kReduceWarps][33];
+    constexpr int U = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     const int n = blockIdx.y ? gk : gq;
@@ -293,26 +422,32 @@ __global__ void __launch_bounds__(256) qk_dw_reduce_kernel(const float* __restri
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float h = 0.f, e = 0.f;
     if (col < D) {
-        for (int i = warp; i < n; i += 64) {
-            float vh[8], vl[8];
+        for (int i = warp; i < n; i += U * kReduceWarps) {
+            float vh[U], vl[U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int k = i + 8 * u;
+            for (int u = 0; u < U; ++u) {
+                const int k = i + kReduceWarps * u;
                 vh[u] = k < n ? __ldcg(p + (int64_t)k * 2 * D + col) : 0.f;
                 vl[u] = k < n ? __ldcg(p + (int64_t)k * 2 * D + D + col) : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) comp_merge(h, e, vh[u], vl[u]);
+            for (int u = 0; u < U; ++u) comp_merge(h, e, vh[u], vl[u]);
         }
     }
     sh[warp][lane] = h;
     sl[warp][lane] = e;
     __syncthreads();
-    if (warp == 0 && col < D) {
+    // a column's 32 sums go to one warp and are merged pairwise
+    h = sh[lane][warp];
+    e = sl[lane][warp];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) comp_merge(h, e, sh[i][lane], sl[i][lane]);
-        (blockIdx.y ? dwk : dwq)[col] = __fadd_rn(h, e);
+    for (int o = 16; o > 0; o >>= 1) {
+        const float ho = __shfl_down_sync(0xffffffffu, h, o);
+        const float eo = __shfl_down_sync(0xffffffffu, e, o);
+        comp_merge(h, e, ho, eo);
     }
+    const int out = blockIdx.x * 32 + warp;
+    if (lane == 0 && out < D) (blockIdx.y ? dwk : dwq)[out] = __fadd_rn(h, e);
 }
 
 template <typename T, int LPR, bool NB>
@@ -358,8 +493,15 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
         units[i] = groups_of(c.tokens, a.span[i], RPW) * a.span[i].parts;
         rows[i] = (int64_t)heads[i];
     }
-    // the CTAs of both sides together are kQkBwdCtasPerSm per SM at most, shared out by rows
-    const int64_t all = (int64_t)c.sms * kQkBwdCtasPerSm;
+    // the CTAs of both sides together are those that are resident at once, shared out by rows
+    Launch L{};
+    L.sms = c.sms;
+    L.grid = (int64_t)c.sms * kQkBwdCtasPerSm;
+    L.smem = sizeof(BwdSmem<T>);
+    int64_t all = 0;
+    auto kernel = qk_bwd_kernel<T, LPR, NB>;
+    cudaError_t e = fit_grid((const void*)kernel, L, kWarps * 32, &all);
+    if (e != cudaSuccess) return e;
     int64_t gk = all * rows[1] / (rows[0] + rows[1]);
     gk = gk < 1 ? 1 : gk;
     int64_t g[2] = {all - gk, gk};
@@ -375,13 +517,13 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
     a.D = c.D;
     a.w_bf16 = c.w_dt;
     a.eps = c.eps;
-    qk_bwd_kernel<T, LPR, NB><<<a.grid[0] + a.grid[1], kWarps * 32, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    kernel<<<a.grid[0] + a.grid[1], kWarps * 32, sizeof(BwdSmem<T>), s>>>(a);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((c.D + 31) / 32), 2);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kReduceWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
