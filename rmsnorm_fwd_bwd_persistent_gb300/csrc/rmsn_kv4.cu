@@ -22,40 +22,71 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+
 // Quantises the 16 neighbouring dims of this lane (two lanes hold a group): two words of eight
 // codes, and the group's scale (low half) and minimum (high half) as bf16.
+//
+// The quotient t/s (t = x - z) is formed as q = t y, y = 1/s rounded, and one step
+// q + y (t - q s), whose remainder is exact (Markstein).  That is within 2^-22 of half a step of
+// t/s, and since s has 8 bits and t 24, t/s is never closer than 2^-9 of a step to the middle
+// between two FP32 numbers: so it is the rounded quotient that a division gives, at a fifth of the
+// instructions.  Scales outside [2^-60, 2^60], where a product could leave the range, divide.
 __device__ __forceinline__ void quantise16(const Raw8<bf16>& a, const Raw8<bf16>& b,
                                            uint32_t (&word)[2], uint32_t& scale_min) {
-    float x[2][8];
-    a.get(x[0]);
-    b.get(x[1]);
-    float mn = x[0][0], mx = x[0][0], odd = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            mn = fminf(mn, x[e][i]);
-            mx = fmaxf(mx, x[e][i]);
-            odd = fmaf(x[e][i], 0.f, odd);  // NaN if any element is not finite
-        }
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    odd += __shfl_xor_sync(0xffffffffu, odd, 1);
-    const bool bad = odd != odd;
+    uint32_t lo = min2(min2(min2(a.a.x, a.a.y), min2(a.a.z, a.a.w)),
+                       min2(min2(b.a.x, b.a.y), min2(b.a.z, b.a.w)));
+    uint32_t up = max2(max2(max2(a.a.x, a.a.y), max2(a.a.z, a.a.w)),
+                       max2(max2(b.a.x, b.a.y), max2(b.a.z, b.a.w)));
+    lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    up = max2(up, __shfl_xor_sync(0xffffffffu, up, 1));
+    lo = min2(lo, __byte_perm(lo, lo, 0x1032));
+    up = max2(up, __byte_perm(up, up, 0x1032));
+    const float mn = bf16_lo(lo), mx = bf16_lo(up);
     const uint32_t sb = bf16_bits(__fsub_rn(__fdiv_rn(mx, 15.f), __fdiv_rn(mn, 15.f)));
     const float s = __uint_as_float(sb << 16);
+    const bool bad = !(fabsf(mn) <= 3.402823466e38f && fabsf(mx) <= 3.402823466e38f);
+    f2 x[2][4];
+    Pairs<bf16>::get(a.a, x[0]);
+    Pairs<bf16>::get(b.a, x[1]);
+    if (s >= 8.67361738e-19f && s <= 1.152921505e18f) {
+        const float y = __frcp_rn(s);
+        const f2 y2 = f2_splat(y), n2 = f2_splat(-s), m2 = f2_splat(mn);
+        const f2 magic = f2_splat(12582912.f);  // 1.5 2^23: the sum's low bits are the integer
+        constexpr uint32_t kMagic = 0x4B400000u * 0x11111111u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t wd = 0u - kMagic;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f2 t = sub2(x[e][i], m2);
+                const f2 q = mul2(t, y2);
+                const f2 c = add2(fma2(fma2(q, n2, t), y2, q), magic);
+                wd += (__float_as_uint(f2_lo(c)) << (8 * i)) + (__float_as_uint(f2_hi(c)) << (8 * i + 4));
+            }
+            word[e] = wd;
+        }
+        scale_min = sb | (lo << 16);
+        return;
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         word[e] = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float c = rintf(__fdiv_rn(__fsub_rn(x[e][i], mn), s));
-            const uint32_t code = s > 0.f ? (uint32_t)fminf(fmaxf(c, 0.f), 15.f) : 0u;
-            word[e] |= code << (4 * i);
+            const float v = i & 1 ? f2_hi(x[e][i / 2]) : f2_lo(x[e][i / 2]);
+            const float c = rintf(__fdiv_rn(__fsub_rn(v, mn), s));
+            if (s > 0.f && !bad) word[e] |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
         }
-        if (bad) word[e] = 0u;
     }
-    scale_min = bad ? 0x7fc07fc0u : sb | (bf16_bits(mn) << 16);
+    scale_min = bad ? 0x7fc07fc0u : sb | (lo << 16);
 }
 
 struct AppendArgs {
@@ -73,7 +104,7 @@ struct AppendArgs {
 
 template <int LPR, bool NB>
 __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArgs a) {
-    constexpr int RPW = 32 / LPR, D = 16 * LPR, U = 2;
+    constexpr int RPW = 32 / LPR, D = 16 * LPR, U = 4;
     __shared__ __align__(16) bf16 turn[kWarps][RPW * D];
     int part = blockIdx.y, side = 0;
     while (side < 2 && part >= a.span[side].parts) part -= a.span[side++].parts;
@@ -147,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
                 for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-                const float rs = row_rstd(row_sum<LPR>(ss), (float)D, a.eps);
+                const float rs = row_rstd(row_sum<LPR>(ss), 1.f / D, a.eps);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     u[e] = u[e] * rs * w0[e];
@@ -214,65 +245,76 @@ struct ReadArgs {
     Span span;
     int64_t pages;
     unsigned* err;
-    int tokens, blocks_per_page;
+    int tokens, blocks_per_page, log_cpt;
 };
+
+// A warp takes U steps of rows at a time: `cpt` chunks of heads (1, 2 or 4) of U / cpt token
+// groups, so as many loads are in flight whatever the number of heads.
+constexpr int kReadSteps = 4;
 
 template <int LPR>
 __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a) {
-    constexpr int RPW = 32 / LPR, D = 16 * LPR, U = 4;
+    constexpr int RPW = 32 / LPR, D = 16 * LPR, U = kReadSteps;
     const Span sp = a.span;
     const int part = blockIdx.y;
     const int lane = threadIdx.x & 31, l = lane % LPR, rr = lane / LPR;
     const int hsub = rr & ((1 << sp.log_hpw) - 1), tsub = rr >> sp.log_hpw;
     const int tpw = RPW >> sp.log_hpw;
-    const int64_t tok = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * tpw + tsub;
-    if (tok >= a.tokens) return;
-    const int64_t slot = __ldg(a.slots + tok);
-    if (slot < 0) return;
-    if (slot >= a.pages * a.blocks_per_page * kKv4Block) {
-        if (part == 0 && l == 0 && hsub == 0) atomicOr(a.err, ERR_INDEX);
-        return;
-    }
-    const uint8_t* rec0 =
-        a.cache + kv4_record(slot, a.pages, a.blocks_per_page, sp.heads, 0) * kv4_record_bytes(D);
+    const int64_t first =
+        ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (U >> a.log_cpt) * tpw + tsub;
     const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
-    const int r = (int)(slot & (kKv4Block - 1));
     const int j = l >> 1;
-    bf16* ko = a.k.row<bf16>(0, (int)tok) + 16 * l;
-    bf16* vo = a.v.row<bf16>(0, (int)tok) + 16 * l;
+    int64_t slot[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int64_t tok = first + (i >> a.log_cpt) * tpw;
+        slot[i] = tok < a.tokens ? __ldg(a.slots + tok) : -1;
+        if (slot[i] >= a.pages * a.blocks_per_page * kKv4Block) {
+            if (part == 0 && l == 0 && hsub == 0) atomicOr(a.err, ERR_INDEX);
+            slot[i] = -1;
+        }
+    }
     const int c1 = min(sp.chunks, (part + 1) * sp.per_part);
-    for (int c = part * sp.per_part; c < c1; c += U) {
+    for (int c0 = part * sp.per_part; c0 < c1; c0 += 1 << a.log_cpt) {
         uint32_t kw[U][2], vw[U][2], ks[U], vs[U];
+        bool ok[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int h = ((c + i) << sp.log_hpw) + hsub;
-            if (c + i >= c1 || h >= sp.heads) continue;
-            const uint8_t* rec = rec0 + h * head_bytes;
+            const int c = c0 + (i & ((1 << a.log_cpt) - 1));
+            const int h = (c << sp.log_hpw) + hsub;
+            ok[i] = slot[i] >= 0 && c < c1 && h < sp.heads;
+            if (!ok[i]) continue;
+            const int r = (int)(slot[i] & (kKv4Block - 1));
+            const uint8_t* rec = a.cache + h * head_bytes +
+                kv4_record(slot[i], a.pages, a.blocks_per_page, sp.heads, 0) * kv4_record_bytes(D);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int wd = 2 * l + e;
-                kw[i][e] = *reinterpret_cast<const uint32_t*>(rec + kv4_k_word(D, r, wd));
-                vw[i][e] = *reinterpret_cast<const uint32_t*>(
-                    rec + kv4_v_unit(D, r, wd / (D / 64)) + 4 * (wd % (D / 64)));
+                kw[i][e] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_k_word(D, r, wd)));
+                vw[i][e] = __ldg(reinterpret_cast<const uint32_t*>(
+                    rec + kv4_v_unit(D, r, wd / (D / 64)) + 4 * (wd % (D / 64))));
             }
-            ks[i] = *reinterpret_cast<const uint32_t*>(rec + kv4_k_scale(D, r, j));
+            ks[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_k_scale(D, r, j)));
             const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, r, j));
-            vs[i] = (uint32_t)p[0] | ((uint32_t)p[2] << 16);
+            vs[i] = (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 2) << 16);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int h = ((c + i) << sp.log_hpw) + hsub;
-            if (c + i >= c1 || h >= sp.heads) continue;
+            if (!ok[i]) continue;
+            const int h = ((c0 + (i & ((1 << a.log_cpt) - 1))) << sp.log_hpw) + hsub;
+            const int tok = (int)(first + (i >> a.log_cpt) * tpw);
+            bf16* ko = a.k.row<bf16>(0, tok) + h * a.k.sh + 16 * l;
+            bf16* vo = a.v.row<bf16>(0, tok) + h * a.v.sh + 16 * l;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float f[8];
                 Raw8<bf16> o;
                 values8(kw[i][e], bf16_lo(ks[i]), bf16_hi(ks[i]), f);
                 o.set(f);
-                o.store(ko + h * a.k.sh + 8 * e);
+                o.store(ko + 8 * e);
                 values8(vw[i][e], bf16_lo(vs[i]), bf16_hi(vs[i]), f);
                 o.set(f);
-                o.store(vo + h * a.v.sh + 8 * e);
+                o.store(vo + 8 * e);
             }
         }
     }
@@ -324,7 +366,9 @@ cudaError_t run_read(const Kv4Read& c, cudaStream_t s) {
     a.err = c.err;
     a.tokens = (int)c.tokens;
     a.blocks_per_page = c.blocks_per_page;
-    const int64_t gx = (groups_of(c.tokens, a.span, RPW) + kWarps - 1) / kWarps;
+    while (a.log_cpt < 2 && (2 << a.log_cpt) <= a.span.per_part) ++a.log_cpt;
+    const int64_t per_cta = (int64_t)kWarps * (kReadSteps >> a.log_cpt);
+    const int64_t gx = (groups_of(c.tokens, a.span, RPW) + per_cta - 1) / per_cta;
     kv4_read_kernel<LPR><<<dim3((unsigned)gx, a.span.parts), kWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
 }

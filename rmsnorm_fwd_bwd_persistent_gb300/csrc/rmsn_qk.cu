@@ -22,6 +22,7 @@ namespace rmsn {
 namespace {
 
 constexpr int kWarps = 4;  // warps per CTA (they are independent)
+constexpr int kBlock = 8;  // dw terms added in FP32 before a compensated addition, at most
 
 struct FwdArgs {
     Heads x[2], y[2];
@@ -58,6 +59,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
     const int64_t sxh = a.x[side].sh, syh = a.y[side].sh;
     const int c1 = min(sp.chunks, (part + 1) * sp.per_part);
 
+    const float inv_d = __frcp_rn((float)a.D);
     Angles ang;
     float w0[8], w1[8];
     bool have = false;
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
             for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            const float r = row_rstd(row_sum<LPR>(ss), (float)a.D, a.eps);
+            const float r = row_rstd(row_sum<LPR>(ss), inv_d, a.eps);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 u[e] = u[e] * r * w0[e];
@@ -129,10 +131,9 @@ struct BwdArgs {
     float eps;
 };
 
-// 16 bytes from global to this lane's own place in shared memory; `bytes` 0 writes zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
+// 16 bytes from global to this lane's own place in shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -180,7 +181,7 @@ __device__ __forceinline__ void store8(T* p, const f2 (&f)[4]) {
 // Persistent: the first grid[0] CTAs take q's units, the others k's; a unit is tpw tokens and
 // one part of their heads (up to 8 chunks).  Rows stream through a ring in shared memory that
 // belongs to the lane alone (asynchronous copies, no barriers), so the bytes in flight do not
-// cost registers.  A lane adds the dw terms of a unit's chunks in FP32, and each unit's sum to
+// cost registers.  A lane adds the dw terms of up to kBlock chunks in FP32 and such sums to
 // a (high, low) pair with TwoSum; the pairs of the CTA's lanes are merged in a fixed order and
 // written to the workspace, whose CTA partials qk_dw_reduce_kernel adds in a fixed order.
 // Two-element FP32 instructions halve the arithmetic.  Measured on GB300 at T = 32768, 32 + 8
@@ -221,15 +222,21 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             sm.sums[0][i][threadIdx.x] = sm.sums[1][i][threadIdx.x] = make_ulonglong2(0ull, 0ull);
         }
     }
-    const int64_t sxh = a.x[side].sh, sgh = a.g[side].sh, sdh = a.dx[side].sh;
+    if (!dims_ok)  // lanes past the row's end add zeros to its sums
+        for (int i = 0; i < S; ++i)
+            for (int v = 0; v < NV; ++v) sm.ring[warp][i][v][lane] = make_uint4(0u, 0u, 0u, 0u);
+    const int hpw = 1 << sp.log_hpw;
+    const int64_t step_x = hpw * a.x[side].sh, step_g = hpw * a.g[side].sh;
+    const int64_t step_d = hpw * a.dx[side].sh;
     const float inv_d = __frcp_rn((float)a.D);
 
-    // A place in the warp's line of chunks.
+    // A place in the warp's line of chunks: the unit, the next head of this row and the end of
+    // the unit's part of them, and the row's token.
     struct At {
         int64_t unit;
         int c, c1, tok;
     };
-    auto enter = [&](At& at) {  // the unit's part of the heads and this row's token
+    auto enter = [&](At& at) {
         const int64_t grp = sp.parts == 1 ? at.unit
                             : (at.unit >> 32) ? at.unit / sp.parts
                                               : (int64_t)((uint32_t)at.unit / (uint32_t)sp.parts);
@@ -238,32 +245,39 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
         at.c1 = min(sp.chunks, at.c + sp.per_part);
         at.tok = (int)min(grp * tpw + tsub, (int64_t)a.tokens);
     };
+    // The copying side runs S - 1 chunks ahead.
     const uint32_t ring = smem_addr(&sm.ring[warp][0][0][lane]);
-    const T *px = nullptr, *pg = nullptr;  // the copying side's rows
+    const T *px0 = nullptr, *px1 = nullptr, *pg0 = nullptr, *pg1 = nullptr;
     At in{(int64_t)cta * kWarps + warp, 0, 0, 0};
     auto rows_in = [&]() {
         if (in.unit >= units) return;
         enter(in);
         const int t = in.tok < a.tokens ? in.tok : 0;
         const int b = a.tokens == a.T ? 0 : t / a.T;
-        px = a.x[side].row<T>(b, t - b * a.T);
-        pg = a.g[side].row<T>(b, t - b * a.T);
+        const int h = (in.c << sp.log_hpw) + hsub;
+        const T* x = a.x[side].row<T>(b, t - b * a.T) + h * a.x[side].sh;
+        const T* g = a.g[side].row<T>(b, t - b * a.T) + h * a.g[side].sh;
+        px0 = x + rl.off0;
+        px1 = x + rl.off1;
+        pg0 = g + rl.off0;
+        pg1 = g + rl.off1;
     };
     auto fetch = [&](int stage) {  // the next chunk, if there is one
         if (in.unit < units) {
-            const int h = (in.c << sp.log_hpw) + hsub;
-            const bool ok = in.tok < a.tokens && dims_ok && h < sp.heads;
-            const uint32_t n = ok ? 16u : 0u;
-            const int64_t hx = ok ? h * sxh : 0, hg = ok ? h * sgh : 0;
-            const uint32_t dst = ring + (uint32_t)stage * (NV * 512);
-            const int o0 = ok ? rl.off0 : 0, o1 = ok ? rl.off1 : 0;
+            if (in.tok < a.tokens && dims_ok && (in.c << sp.log_hpw) + hsub < sp.heads) {
+                const uint32_t dst = ring + (uint32_t)stage * (NV * 512);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                copy16(dst + i * 512, px + hx + o0 + 4 * i, n);
-                copy16(dst + (V + i) * 512, px + hx + o1 + 4 * i, n);
-                copy16(dst + (2 * V + i) * 512, pg + hg + o0 + 4 * i, n);
-                copy16(dst + (3 * V + i) * 512, pg + hg + o1 + 4 * i, n);
+                for (int i = 0; i < V; ++i) {
+                    copy16(dst + i * 512, px0 + 4 * i);
+                    copy16(dst + (V + i) * 512, px1 + 4 * i);
+                    copy16(dst + (2 * V + i) * 512, pg0 + 4 * i);
+                    copy16(dst + (3 * V + i) * 512, pg1 + 4 * i);
+                }
             }
+            px0 += step_x;
+            px1 += step_x;
+            pg0 += step_g;
+            pg1 += step_g;
             if (++in.c == in.c1) {
                 in.unit += stride;
                 rows_in();
@@ -275,23 +289,42 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) fetch(i);
 
-    int stage = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ulonglong2 hi = sm.sums[0][i][threadIdx.x], lo = sm.sums[1][i][threadIdx.x];
+            f2 h0 = hi.x, l0 = lo.x, h1 = hi.y, l1 = lo.y;
+            comp_add2(h0, l0, acc[2 * i]);
+            comp_add2(h1, l1, acc[2 * i + 1]);
+            sm.sums[0][i][threadIdx.x] = make_ulonglong2(h0, h1);
+            sm.sums[1][i][threadIdx.x] = make_ulonglong2(l0, l1);
+            acc[2 * i] = acc[2 * i + 1] = 0ull;
+        }
+    };
+    int stage = 0, added = 0;
     for (At at{(int64_t)cta * kWarps + warp, 0, 0, 0}; at.unit < units; at.unit += stride) {
         enter(at);
         const Token tk = find_token(at.tok, a.tokens, a.T, a.rope, a.err,
                                     side == 0 && at.c == 0 && l == 0 && hsub == 0);
         const bool ok = tk.ok && dims_ok;
-        T* dx = a.dx[side].row<T>(tk.b, tk.t);
         Angles ang;
         ang.identity();
         if (ok && rl.turns) {
             const int64_t p = tk.pos * (a.rope.rd / 2) + 8 * l;
             ang.load(a.rope.cos + p, a.rope.sin + p);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0ull;
+        int h = (at.c << sp.log_hpw) + hsub;
+        T* d0 = a.dx[side].row<T>(tk.b, tk.t) + h * a.dx[side].sh;
+        T* d1 = d0 + rl.off1;
+        d0 += rl.off0;
+        if (added + at.c1 - at.c > kBlock) {
+            flush();
+            added = 0;
+        }
+        added += at.c1 - at.c;
         for (int c = at.c; c < at.c1; ++c) {
-            const int h = (c << sp.log_hpw) + hsub;
             copy_wait<S - 2>();
             const uint4* slot = &sm.ring[warp][stage][0][lane];
             f2 x0[4], x1[4], h0[4], h1[4];
@@ -323,10 +356,9 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
                 for (int i = 0; i < 4; ++i) {
                     const f2 cc = f2_make(ang.c[2 * i], ang.c[2 * i + 1]);
                     const f2 s2 = f2_make(ang.s[2 * i], ang.s[2 * i + 1]);
-                    const f2 n2 = f2_make(-ang.s[2 * i], -ang.s[2 * i + 1]);
                     const f2 y = h0[i];
                     h0[i] = fma2(h1[i], s2, mul2(y, cc));
-                    h1[i] = fma2(y, n2, mul2(h1[i], cc));
+                    h1[i] = sub2(mul2(h1[i], cc), mul2(y, s2));
                 }
             }
             f2 ss2 = 0ull, dot2 = 0ull;
@@ -342,35 +374,32 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             }
             const float ss = row_sum<LPR>(f2_lo(ss2) + f2_hi(ss2));
             const float dot = row_sum<LPR>(f2_lo(dot2) + f2_hi(dot2));
-            const float r = row_rstd(ss, (float)a.D, a.eps);
-            // dx = r (h w) - x r k,  k = r^2 mean(g x)
+            const float r = row_rstd(ss, inv_d, a.eps);
+            // dx = (h r) w - x r k,  k = r^2 mean(g x);  dw += (h r) x
             const f2 r2 = f2_splat(r), nk = f2_splat(-(r * (r * (r * (dot * inv_d)))));
             if (ok && h < sp.heads) {
                 f2 d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[i] = fma2(h0[i], mul2(x0[i], r2), acc[i]);
-                    d[i] = fma2(x0[i], nk, mul2(mul2(h0[i], w0[i]), r2));
+                    const f2 hr = mul2(h0[i], r2);
+                    acc[i] = fma2(hr, x0[i], acc[i]);
+                    d[i] = fma2(x0[i], nk, mul2(hr, w0[i]));
                 }
-                store8<T>(dx + h * sdh + rl.off0, d);
+                store8<T>(d0, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[4 + i] = fma2(h1[i], mul2(x1[i], r2), acc[4 + i]);
-                    d[i] = fma2(x1[i], nk, mul2(mul2(h1[i], w1[i]), r2));
+                    const f2 hr = mul2(h1[i], r2);
+                    acc[4 + i] = fma2(hr, x1[i], acc[4 + i]);
+                    d[i] = fma2(x1[i], nk, mul2(hr, w1[i]));
                 }
-                store8<T>(dx + h * sdh + rl.off1, d);
+                store8<T>(d1, d);
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ulonglong2 hi = sm.sums[0][i][threadIdx.x], lo = sm.sums[1][i][threadIdx.x];
-            f2 h0 = hi.x, l0 = lo.x, h1 = hi.y, l1 = lo.y;
-            comp_add2(h0, l0, acc[2 * i]);
-            comp_add2(h1, l1, acc[2 * i + 1]);
-            sm.sums[0][i][threadIdx.x] = make_ulonglong2(h0, h1);
-            sm.sums[1][i][threadIdx.x] = make_ulonglong2(l0, l1);
+            h += hpw;
+            d0 += step_d;
+            d1 += step_d;
         }
     }
+    flush();
     copy_wait<0>();
     __syncthreads();
 

@@ -137,9 +137,16 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// 1/sqrt(ss/D + eps), IEEE operations (rd: 1/D rounded is not used, the mean is a division).
-__device__ __forceinline__ float row_rstd(float ss, float D, float eps) {
-    return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, D), eps)));
+// 1/sqrt(ss/D + eps) for inv_d = 1/D: the hardware's approximation (2^-22.9 relative) and one
+// Newton step r + r/2 (1 - m r^2), which leaves about one rounding; the IEEE divide, square root
+// and reciprocal are four times the instructions.  A sum of squares beyond FP32 gives 0, as in
+// the row kernels.
+__device__ __forceinline__ float row_rstd(float ss, float inv_d, float eps) {
+    const float m = fmaf(ss, inv_d, eps);
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(m));
+    r = fmaf(0.5f * r, fmaf(-(m * r), r, 1.f), r);
+    return m > 3.402823466e38f ? 0.f : r;
 }
 
 // One operand of the kernels: the rows of q, k or v in memory.  Strides in elements.
