@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
     const int c1 = min(sp.chunks, (part + 1) * sp.per_part);
     uint8_t* rec0 = a.cache;
     if (ok && side > 0)
-        rec0 += kv4_record(slot, a.pages, a.blocks_per_page, a.kv_heads, 0) * kv4_record_bytes(D);
+        rec0 += kv4_record_of(slot, a.blocks_per_page, a.kv_heads) * kv4_record_bytes(D);
     const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
     const int r = (int)(slot & (kKv4Block - 1));
 
@@ -232,6 +232,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
     }
 }
 
+__device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
+    return __ldg(reinterpret_cast<const uint32_t*>(p));
+}
+
 // Eight codes, scale and minimum -> eight values.
 __device__ __forceinline__ void values8(uint32_t word, float s, float z, float (&f)[8]) {
 #pragma unroll
@@ -249,7 +253,8 @@ struct ReadArgs {
 };
 
 // A warp takes U steps of rows at a time: `cpt` chunks of heads (1, 2 or 4) of U / cpt token
-// groups, so as many loads are in flight whatever the number of heads.
+// groups, so as many loads are in flight whatever the number of heads.  Lane l of a row takes the
+// dims 8l .. 8l + 7 of each half of the head, so that a store of the warp writes whole rows.
 constexpr int kReadSteps = 4;
 
 template <int LPR>
@@ -263,58 +268,59 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
     const int64_t first =
         ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (U >> a.log_cpt) * tpw + tsub;
     const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
-    const int j = l >> 1;
-    int64_t slot[U];
+    const uint8_t* rec0[U];  // the record of head 0; null: nothing to do
+    int row[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int64_t tok = first + (i >> a.log_cpt) * tpw;
-        slot[i] = tok < a.tokens ? __ldg(a.slots + tok) : -1;
-        if (slot[i] >= a.pages * a.blocks_per_page * kKv4Block) {
+        const int64_t slot = tok < a.tokens ? __ldg(a.slots + tok) : -1;
+        rec0[i] = nullptr;
+        row[i] = (int)(slot & (kKv4Block - 1));
+        if (slot >= a.pages * a.blocks_per_page * kKv4Block) {
             if (part == 0 && l == 0 && hsub == 0) atomicOr(a.err, ERR_INDEX);
-            slot[i] = -1;
+        } else if (slot >= 0) {
+            rec0[i] = a.cache + kv4_record_of(slot, a.blocks_per_page, sp.heads) *
+                                    kv4_record_bytes(D);
         }
     }
     const int c1 = min(sp.chunks, (part + 1) * sp.per_part);
     for (int c0 = part * sp.per_part; c0 < c1; c0 += 1 << a.log_cpt) {
-        uint32_t kw[U][2], vw[U][2], ks[U], vs[U];
+        uint32_t kw[U][2], vw[U][2], ks[U][2], vs[U][2];
         bool ok[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int c = c0 + (i & ((1 << a.log_cpt) - 1));
             const int h = (c << sp.log_hpw) + hsub;
-            ok[i] = slot[i] >= 0 && c < c1 && h < sp.heads;
+            ok[i] = rec0[i] && c < c1 && h < sp.heads;
             if (!ok[i]) continue;
-            const int r = (int)(slot[i] & (kKv4Block - 1));
-            const uint8_t* rec = a.cache + h * head_bytes +
-                kv4_record(slot[i], a.pages, a.blocks_per_page, sp.heads, 0) * kv4_record_bytes(D);
+            const uint8_t* rec = rec0[i] + h * head_bytes;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int wd = 2 * l + e;
-                kw[i][e] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_k_word(D, r, wd)));
-                vw[i][e] = __ldg(reinterpret_cast<const uint32_t*>(
-                    rec + kv4_v_unit(D, r, wd / (D / 64)) + 4 * (wd % (D / 64))));
+                const int wd = l + LPR * e, j = wd >> 2;
+                kw[i][e] = ldg_word(rec + kv4_k_word(D, row[i], wd));
+                vw[i][e] = ldg_word(rec + kv4_v_unit(D, row[i], wd / (D / 64)) + 4 * (wd % (D / 64)));
+                ks[i][e] = ldg_word(rec + kv4_k_scale(D, row[i], j));
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, row[i], j));
+                vs[i][e] = (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 2) << 16);
             }
-            ks[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + kv4_k_scale(D, r, j)));
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, r, j));
-            vs[i] = (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 2) << 16);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (!ok[i]) continue;
             const int h = ((c0 + (i & ((1 << a.log_cpt) - 1))) << sp.log_hpw) + hsub;
             const int tok = (int)(first + (i >> a.log_cpt) * tpw);
-            bf16* ko = a.k.row<bf16>(0, tok) + h * a.k.sh + 16 * l;
-            bf16* vo = a.v.row<bf16>(0, tok) + h * a.v.sh + 16 * l;
+            bf16* ko = a.k.row<bf16>(0, tok) + h * a.k.sh + 8 * l;
+            bf16* vo = a.v.row<bf16>(0, tok) + h * a.v.sh + 8 * l;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float f[8];
                 Raw8<bf16> o;
-                values8(kw[i][e], bf16_lo(ks[i]), bf16_hi(ks[i]), f);
+                values8(kw[i][e], bf16_lo(ks[i][e]), bf16_hi(ks[i][e]), f);
                 o.set(f);
-                o.store(ko + 8 * e);
-                values8(vw[i][e], bf16_lo(vs[i]), bf16_hi(vs[i]), f);
+                st_stream(ko + D / 2 * e, o.a);
+                values8(vw[i][e], bf16_lo(vs[i][e]), bf16_hi(vs[i][e]), f);
                 o.set(f);
-                o.store(vo + 8 * e);
+                st_stream(vo + D / 2 * e, o.a);
             }
         }
     }

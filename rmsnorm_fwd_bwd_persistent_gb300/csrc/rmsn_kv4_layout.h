@@ -58,12 +58,19 @@ RMSN_HD int kv4_v_scale(int D, int r, int j) {
     return 18 * D + (r >> 1) * (D / 4) + 8 * j + 2 * (r & 1);
 }
 
-// Record of a token's slot (slot = page * page_size + offset) and head; -1 outside the cache.
-RMSN_HD int64_t kv4_record(int64_t slot, int64_t pages, int blocks_per_page, int kv_heads, int h) {
+// Record of head 0 of a slot (slot = page * page_size + offset) that is inside the cache; head h
+// is h * blocks_per_page records on.
+RMSN_HD int64_t kv4_record_of(int64_t slot, int blocks_per_page, int kv_heads) {
     const int64_t block = slot >> 4;
-    if (slot < 0 || block >= pages * blocks_per_page) return -1;
-    const int64_t page = block / blocks_per_page;
-    return (page * kv_heads + h) * blocks_per_page + (block - page * blocks_per_page);
+    const int64_t page = block >> 31 ? block / blocks_per_page
+                                     : (int64_t)((uint32_t)block / (uint32_t)blocks_per_page);
+    return page * (kv_heads - 1) * blocks_per_page + block;
+}
+
+// Record of any slot and head; -1 outside the cache.
+RMSN_HD int64_t kv4_record(int64_t slot, int64_t pages, int blocks_per_page, int kv_heads, int h) {
+    if (slot < 0 || (slot >> 4) >= pages * blocks_per_page) return -1;
+    return kv4_record_of(slot, blocks_per_page, kv_heads) + (int64_t)h * blocks_per_page;
 }
 
 }  // namespace rmsn
