@@ -484,7 +484,7 @@ int qk_norm_rope_kv4_append(const rmsn_heads_t* q, const rmsn_heads_t* k, const 
                             rmsn_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
- * kv4_read -- K and V of any slots as bf16 (c * s + z in FP32, rounded once): the inverse of
+ * kv4_read -- K and V of any slots as bf16 (c * s + z, rounded once): the inverse of
  * the append, e.g. for a dense attention over a cached prefix.  k and v are outputs of
  * [T, kv_heads, D] by strides.  Rows of a negative slot stay as they were; so do those of a
  * slot beyond the cache, which sets bit 3.

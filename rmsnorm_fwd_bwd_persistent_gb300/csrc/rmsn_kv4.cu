@@ -236,10 +236,18 @@ __device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
     return __ldg(reinterpret_cast<const uint32_t*>(p));
 }
 
-// Eight codes, scale and minimum -> eight values.
-__device__ __forceinline__ void values8(uint32_t word, float s, float z, float (&f)[8]) {
+// Eight codes -> eight bf16 values c s + z, one rounding each (s and z twice in their words).
+// 128 + c is a bf16 with the code in its low bits, so c comes out exactly; the FMA rounds.
+__device__ __forceinline__ uint4 values8(uint32_t word, uint32_t s2, uint32_t z2) {
+    uint32_t v[4];  // dims (i, i + 4)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf((float)((word >> (4 * i)) & 15u), s, z);
+    for (int i = 0; i < 4; ++i) {
+        v[i] = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x43004300u));
+        asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(v[i]) : "r"(s2), "r"(z2));
+    }
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                      __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
 struct ReadArgs {
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
                 vw[i][e] = ldg_word(rec + kv4_v_unit(D, row[i], wd / (D / 64)) + 4 * (wd % (D / 64)));
                 ks[i][e] = ldg_word(rec + kv4_k_scale(D, row[i], j));
                 const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, row[i], j));
-                vs[i][e] = (uint32_t)__ldg(p) | ((uint32_t)__ldg(p + 2) << 16);
+                vs[i][e] = __byte_perm(__ldg(p), __ldg(p + 2), 0x5410);
             }
         }
 #pragma unroll
@@ -313,14 +321,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
             bf16* vo = a.v.row<bf16>(0, tok) + h * a.v.sh + 8 * l;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float f[8];
-                Raw8<bf16> o;
-                values8(kw[i][e], bf16_lo(ks[i][e]), bf16_hi(ks[i][e]), f);
-                o.set(f);
-                st_stream(ko + D / 2 * e, o.a);
-                values8(vw[i][e], bf16_lo(vs[i][e]), bf16_hi(vs[i][e]), f);
-                o.set(f);
-                st_stream(vo + D / 2 * e, o.a);
+                st_stream(ko + D / 2 * e, values8(kw[i][e], __byte_perm(ks[i][e], 0, 0x1010),
+                                                  __byte_perm(ks[i][e], 0, 0x3232)));
+                st_stream(vo + D / 2 * e, values8(vw[i][e], __byte_perm(vs[i][e], 0, 0x1010),
+                                                  __byte_perm(vs[i][e], 0, 0x3232)));
             }
         }
     }
