@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ctas = gridDim.x;
+    asm volatile("griddepcontrol.launch_dependents;");  // the combine waits for this grid's end
 
     if (threadIdx.x == 0) {
         for (int w = 0; w < kWarps; ++w)
@@ -752,18 +753,23 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 atomicOr(a.err, ERR_WAIT_DRAIN);
 }
 
-// Rows (query token blockIdx.x, head blockIdx.y) whose item lies in several CTAs, or has no
-// tokens at all.  D/4 lanes hold the row; the 1024/D groups of lanes take the CTAs' partial sums
-// in turn, four loads at a time, and are merged in order.
+// Rows (query token, head) whose item lies in several CTAs, or has no tokens at all.  D/4 lanes
+// hold a row.  WIDE: a CTA per row, whose 1024/D groups of lanes take the partial sums in turn
+// and are merged in order; otherwise each group has a row of its own (items that lie in a few
+// CTAs only).
 constexpr int kCombineThreads = 256;
 
-template <int D, int NT>
+template <int D, int NT, bool WIDE>
 __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args a, int ctas) {
     constexpr int QC = 8 * NT, LN = D / 4, GR = kCombineThreads / LN, U = 4;
-    __shared__ float4 so[GR][LN];
+    constexpr int STEP = WIDE ? GR : 1;
+    __shared__ float4 so[WIDE ? GR : 1][LN];
     __shared__ float smx[GR], sl[GR];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int row = blockIdx.x, hq = blockIdx.y, h = hq / a.group;
+    const int ln = threadIdx.x % LN, gr = threadIdx.x / LN;
+    const int64_t at_row = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * GR + gr;
+    const bool in = at_row < (int64_t)a.tokens * a.heads;
+    const int row = in ? (int)at_row / a.heads : 0, hq = in ? (int)at_row - row * a.heads : 0;
+    const int h = a.over_group(hq);
     int b = row;
     if (a.cu_q) {  // the last sequence that starts at or before the row
         int lo = 0, hi = a.seqs;
@@ -774,31 +780,35 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
         }
         b = lo;
     }
-    if (b >= a.seqs) return;
     const Seq s = seq_of<QC>(a, b, false);
-    if (row < s.q0 || row >= s.q0 + s.n) return;
+    // every CTA waits here: what is launched next relies on this grid's end being the other's too
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!in || row < s.q0 || row >= s.q0 + s.n) return;
     const int idx = (row - s.q0) * a.group + hq - h * a.group;
     const int qb = idx / QC, col = idx - qb * QC;
-    const int ln = threadIdx.x % LN, gr = threadIdx.x / LN;
     bf16* out = a.out + (int64_t)row * a.out_st + (int64_t)hq * a.out_sh;
+    float* lse = a.lse ? a.lse + at_row : nullptr;
     if (s.units == 0) {
-        if (gr == 0) *reinterpret_cast<uint2*>(out + 4 * ln) = make_uint2(0u, 0u);
-        if (threadIdx.x == 0 && a.lse)
-            a.lse[(int64_t)row * a.heads + hq] = -__int_as_float(0x7f800000);
+        if (!WIDE || gr == 0) {
+            *reinterpret_cast<uint2*>(out + 4 * ln) = make_uint2(0u, 0u);
+            if (ln == 0 && lse) *lse = -__int_as_float(0x7f800000);
+        }
         return;
     }
     const int64_t per = share_of(a.prefix[a.seqs], ctas);
     const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * s.units;
-    const int c0 = (int)(u0 / per), c1 = (int)((u0 + s.units - 1) / per);
+    const int64_t u1 = u0 + s.units - 1;
+    const int c0 = u1 >> 32 ? (int)(u0 / per) : (int)((uint32_t)u0 / (uint32_t)per);
+    const int c1 = u1 >> 32 ? (int)(u1 / per) : (int)((uint32_t)u1 / (uint32_t)per);
     if (c0 == c1) return;
     float m = -FLT_MAX, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + gr; c <= c1; c += U * GR) {
+    for (int c = c0 + (WIDE ? gr : 0); c <= c1; c += U * STEP) {
         float2 ml[U];
         float4 o[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int64_t cta = c + i * GR;
+            const int64_t cta = c + i * STEP;
             ml[i] = make_float2(-FLT_MAX, 0.f);
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (cta <= c1) {
@@ -819,33 +829,34 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
             v.w = fmaf(e1, o[i].w, e0 * v.w);
         }
     }
-    so[gr][ln] = v;
-    if (ln == 0) {
-        smx[gr] = m;
-        sl[gr] = l;
-    }
-    __syncthreads();
-    if (gr != 0) return;
+    if (WIDE) {
+        so[gr][ln] = v;
+        if (ln == 0) {
+            smx[gr] = m;
+            sl[gr] = l;
+        }
+        __syncthreads();
+        if (gr != 0) return;
 #pragma unroll
-    for (int k = 1; k < GR; ++k) m = fmaxf(m, smx[k]);
-    l = 0.f;
-    v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 1; k < GR; ++k) m = fmaxf(m, smx[k]);
+        l = 0.f;
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < GR; ++k) {
-        const float e = ex2(smx[k] - m);
-        const float4 o = so[k][ln];
-        l = fmaf(e, sl[k], l);
-        v.x = fmaf(e, o.x, v.x);
-        v.y = fmaf(e, o.y, v.y);
-        v.z = fmaf(e, o.z, v.z);
-        v.w = fmaf(e, o.w, v.w);
+        for (int k = 0; k < GR; ++k) {
+            const float e = ex2(smx[k] - m);
+            const float4 o = so[k][ln];
+            l = fmaf(e, sl[k], l);
+            v.x = fmaf(e, o.x, v.x);
+            v.y = fmaf(e, o.y, v.y);
+            v.z = fmaf(e, o.z, v.z);
+            v.w = fmaf(e, o.w, v.w);
+        }
     }
     const float inv = l == 0.f ? 0.f : __frcp_rn(l);
     *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln)) = pack_bf16x2(v.x * inv, v.y * inv);
     *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln + 1)) = pack_bf16x2(v.z * inv, v.w * inv);
-    if (ln == 0 && a.lse)
-        a.lse[(int64_t)row * a.heads + hq] = l == 0.f ? -__int_as_float(0x7f800000)
-                                                       : (m + log2f(l)) * 0.693147180559945309f;
+    if (ln == 0 && lse)
+        *lse = l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 int64_t prefix_bytes(int seqs) { return ((int64_t)(seqs + 1) * 8 + 255) / 256 * 256; }
@@ -897,8 +908,12 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
+    // an item lies in about grid / items CTAs (all of the same length): from 8 on, a CTA per row
+    const int64_t rows = (int64_t)c.tokens * c.heads, items = (int64_t)c.seqs * c.kv_heads;
+    const bool wide = grid >= 8 * items;
+    const int per_cta = wide ? 1 : kCombineThreads * 4 / D;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)c.tokens, (unsigned)c.heads);
+    cfg.gridDim = dim3((unsigned)((rows + per_cta - 1) / per_cta));
     cfg.blockDim = dim3(kCombineThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -906,7 +921,8 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT>, (const Args)a, (int)grid);
+    return wide ? cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT, true>, (const Args)a, (int)grid)
+                : cudaLaunchKernelEx(&cfg, kv4_combine_kernel<D, NT, false>, (const Args)a, (int)grid);
 }
 
 }  // namespace

@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
     constexpr int RPW = 32 / LPR, S = Sm::S, V = Sm::V, NV = Sm::NV;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
+    asm volatile("griddepcontrol.launch_dependents;");  // the reduce waits for this grid's end
     const int side = (int)blockIdx.x < a.grid[0] ? 0 : 1;
     const int cta = blockIdx.x - (side ? a.grid[0] : 0);
     const Span sp = a.span[side];
@@ -443,7 +444,7 @@ constexpr int kReduceWarps = 32;
 __global__ void __launch_bounds__(kReduceWarps * 32)
     qk_dw_reduce_kernel(const float* __restrict__ ws, float* dwq, float* dwk, int D, int gq, int gk) {
     __shared__ float sh[kReduceWarps][33], sl[kReduceWarps][33];
-    constexpr int U = 4;
+    constexpr int U = 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     const int n = blockIdx.y ? gk : gq;
@@ -512,7 +513,7 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
     BwdArgs a{};
     const int heads[2] = {c.heads[0], c.heads[1]};
     const int per = pick_per_part(heads, 2, c.tokens, RPW, c.sms);
-    int64_t units[2], rows[2];
+    int64_t units[2], work[2];
     for (int i = 0; i < 2; ++i) {
         a.x[i] = c.x[i];
         a.g[i] = c.g[i];
@@ -520,9 +521,12 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
         a.w[i] = c.w[i];
         a.span[i] = make_span(heads[i], RPW, per);
         units[i] = groups_of(c.tokens, a.span[i], RPW) * a.span[i].parts;
-        rows[i] = (int64_t)heads[i];
+        work[i] = units[i] * (2 * a.span[i].per_part + 3);
     }
-    // the CTAs of both sides together are those that are resident at once, shared out by rows
+    // The CTAs of both sides together are those that are resident at once, shared out by the
+    // work: a unit's chunks, and about one and a half chunks' time for entering it (angles,
+    // pointers, sums).  Measured with 32 + 8 heads of 128 (bf16), T = 8192 / 32768: shared out by
+    // rows 54.5 / 207 us, waiting for k's units of two chunks; by work 46.1 / 170 us.
     Launch L{};
     L.sms = c.sms;
     L.grid = (int64_t)c.sms * kQkBwdCtasPerSm;
@@ -531,8 +535,8 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
     auto kernel = qk_bwd_kernel<T, LPR, NB>;
     cudaError_t e = fit_grid((const void*)kernel, L, kWarps * 32, &all);
     if (e != cudaSuccess) return e;
-    int64_t gk = all * rows[1] / (rows[0] + rows[1]);
-    gk = gk < 1 ? 1 : gk;
+    int64_t gk = (int64_t)((double)all * work[1] / ((double)work[0] + work[1]) + 0.5);
+    gk = gk < 1 ? 1 : gk > all - 1 ? all - 1 : gk;
     int64_t g[2] = {all - gk, gk};
     for (int i = 0; i < 2; ++i) {
         const int64_t need = (units[i] + kWarps - 1) / kWarps;
