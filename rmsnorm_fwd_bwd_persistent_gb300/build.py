@@ -1,8 +1,10 @@
-"""Builds the CUDA library ``librmsn_gb300.so`` in-tree for sm_103a with nvcc.
+"""Builds the CUDA library ``librmsn_gb300.so`` in-tree for sm_103a with nvcc, and the
+CPython module ``_binding.so`` (the tensor side of the attention entry points) with g++.
 
-The translation units compile in parallel (one nvcc per file) and are linked into one
+The translation units compile in parallel (one compiler per file) and are linked into one
 shared library with the CUDA runtime linked statically, so the library depends only on
-the driver.  No fast-math: IEEE division and square root, no flush-to-zero.
+the driver.  No fast-math: IEEE division and square root, no flush-to-zero.  The module is
+linked against the library and the torch it is built with.
 
 Usage: ``python -m rmsnorm_fwd_bwd_persistent_gb300.build [--verbose-ptxas]``
 """
@@ -20,6 +22,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librmsn_gb300.so")
+
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SOURCE = "rmsn_binding.cpp"
 
 SOURCES = ["rmsn_api.cu", "rmsn_fwd.cu", "rmsn_bwd.cu", "rmsn_bwd_small.cu",
            "rmsn_fused_quant.cu", "rmsn_qk.cu", "rmsn_kv4.cu", "rmsn_kv4_attn.cu",
@@ -47,10 +52,34 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _binding_flags() -> tuple[list[str], list[str]]:
+    """Compile and link flags of the module: the headers and libraries of the installed torch."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    lib = os.path.join(base, "lib")
+    compile_ = ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
+                "-isystem", os.path.join(cuda, "include"),
+                "-isystem", sysconfig.get_paths()["include"]]
+    link = ["-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
@@ -60,26 +89,29 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
 
-    def compile_one(src: str) -> tuple[str, str]:
-        obj = os.path.join(BUILD, src.replace(".cu", ".o"))
-        cmd = [nvcc, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-        return obj, r.stderr
+    cxx = shutil.which("g++") or "g++"
+    cxx_flags, cxx_link = _binding_flags()
 
-    with cf.ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    def compile_one(src: str) -> tuple[str, str]:
+        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        path = os.path.join(CSRC, src)
+        cmd = [cxx, *cxx_flags, "-c", path, "-o", obj] if src == BINDING_SOURCE else \
+            [nvcc, *NVCC_FLAGS, *extra, "-c", path, "-o", obj]
+        return obj, _run(cmd, f"compiling {src}")
+
+    sources = SOURCES + [BINDING_SOURCE]
+    with cf.ThreadPoolExecutor(max_workers=jobs or len(sources)) as ex:
+        results = list(ex.map(compile_one, sources))
     if verbose_ptxas:
         for (_, log) in results:
             sys.stderr.write(log)
     objs = [o for o, _ in results]
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs[:-1]], "linking the library")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run([cxx, "-shared", "-o", tmp, objs[-1], *cxx_link], "linking the module")
+    os.replace(tmp, BINDING)
     return LIB
 
 
