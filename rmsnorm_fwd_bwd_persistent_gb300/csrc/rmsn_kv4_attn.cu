@@ -27,9 +27,11 @@
 // is the output's own rounding); its range is given by a running power of two per group, 2^k,
 // that rises when a scale or minimum needs it.  Sums, references and outputs are FP32.
 //
-// Work split.  Units of 32 tokens of all (sequence, kv head) items form one line that is cut
+// Work split.  Units of 32 tokens of all (sequence, kv head) items form one line, each item
+// with kItemCost places before its units for what entering and merging it costs; the line is cut
 // into equal shares, one per CTA, so ragged batches and single long sequences load all SMs
-// alike; a CTA's four warps take the units of an item in turn, each streaming its own through
+// alike.  (Without those places CTAs that got many short items were late: 64 sequences of up to
+// 500 tokens took 35 us, 16 of up to 2000, the same tokens, 16.)  A CTA's four warps take the units of an item in turn, each streaming its own through
 // a ring in shared memory (bulk copies of whole records), and merge at the item's end.  An item
 // that lies in several CTAs leaves partial sums in the workspace, which kv4_combine_kernel adds
 // in CTA order: results do not depend on timing.
@@ -47,7 +49,8 @@ using bf16 = __nv_bfloat16;
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;      // at most (sizes the workspace)
 constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
-constexpr int kMinShare = kWarps;  // least units per CTA: one for each warp
+constexpr int kMinShare = kWarps;  // least share of a CTA: a unit for each warp
+constexpr int kItemCost = 8;  // what entering and merging an item costs, in units
 
 // Ring stages of one unit per warp (two are 160 KiB in flight per SM at D = 128 and 256), and
 // the CTAs per SM that the registers are divided among.
@@ -66,7 +69,7 @@ struct Args {
     int64_t table_stride;
     const int* kv_lens;
     const int* cu_q;
-    int64_t* prefix;  // [seqs + 1] first unit of every sequence
+    int64_t* prefix;  // [seqs + 1] first place of every sequence
     float* part;      // [CTA][2][columns][D]
     float2* part_ml;  // [CTA][2][columns] (maximum, sum)
     unsigned* err;
@@ -105,8 +108,12 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool report) {
     return s;
 }
 
-__device__ __forceinline__ int64_t share_of(int64_t units, int ctas) {
-    const int64_t up = units + ctas - 1;
+// Places of one sequence's items on the line, and places per CTA.
+__device__ __forceinline__ int64_t places_of(const Seq& s, int kv_heads) {
+    return s.units ? (int64_t)(s.units + kItemCost) * s.qblocks * kv_heads : 0;
+}
+__device__ __forceinline__ int64_t share_of(int64_t places, int ctas) {
+    const int64_t up = places + ctas - 1;
     const int64_t per = up >> 32 ? up / ctas : (int64_t)((uint32_t)up / (uint32_t)ctas);
     return per < kMinShare ? kMinShare : per;
 }
@@ -200,8 +207,6 @@ struct Smem {
     } w[kWarps];
     float m[kWarps][QC], l[kWarps][QC];
     uint64_t full[kWarps][S];
-    int64_t sum[kWarps], found;
-    int found_seq;
 };
 
 // First of the two dims in the n-th pair of a row of sums: pairs run over g, then over the
@@ -209,6 +214,16 @@ struct Smem {
 template <int D>
 __device__ __forceinline__ int dim_of(int n) {
     return (n & 7) * (D / 8) + 2 * (n >> 3);
+}
+
+// Writes the n-th four of a row's sums divided by l, and at n = 0 the log of the sum.
+template <int D>
+__device__ __forceinline__ void put_row(bf16* out, float* lse, int n, float4 v, float m, float l) {
+    const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * n)) = pack_bf16x2(v.x * inv, v.y * inv);
+    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * n + 1)) = pack_bf16x2(v.z * inv, v.w * inv);
+    if (n == 0 && lse)
+        *lse = l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.693147180559945309f;
 }
 
 // The columns' state of one warp over one item.
@@ -252,9 +267,9 @@ struct Warp {
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // the row's largest becomes 2^14 .. 2^15 (in two factors: the power may be beyond FP32)
-            const int ex = amax > 0.f && amax <= FLT_MAX ? exponent(amax) - 15 : 0;
-            const float p1 = pow2(-ex / 2), p2 = pow2(-ex - -ex / 2);
+            // the row's largest becomes 2^14 .. 2^15 (unless it is below 2^-85)
+            const int ex = amax > 0.f && amax <= FLT_MAX ? max(exponent(amax) - 15, -100) : 0;
+            const float p0 = pow2(-ex), p1 = pow2(-ex - 4);
             float z[NG];
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
@@ -266,8 +281,8 @@ struct Warp {
                 z[j] *= a.scale_log2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float d = e & 1 ? 0.0625f : 1.f;
-                    qf[nt][j][e] = pack_f16x2(x[j][e] * p1 * p2 * d, x[j][e + 4] * p1 * p2 * d);
+                    const float p = e & 1 ? p1 : p0;
+                    qf[nt][j][e] = pack_f16x2(x[j][e] * p, x[j][e + 4] * p);
                 }
             }
             // the lane's two groups of the minima's product, each sum as three bf16 terms
@@ -297,8 +312,7 @@ struct Warp {
                 qz[nt][NZ - 1][0] = term[2];
                 qz[nt][NZ - 1][1] = 0u;
             }
-            // a power beyond FP32 belongs to scores beyond it
-            const float fac = a.scale_log2 * pow2((ex + 24) / 2) * pow2(ex + 24 - (ex + 24) / 2);
+            const float fac = a.scale_log2 * pow2(ex + 24);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 f[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * c);  // of column 2t + c
@@ -546,8 +560,6 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     extern __shared__ __align__(128) uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ctas = gridDim.x;
-    asm volatile("griddepcontrol.launch_dependents;");  // the combine waits for this grid's end
 
     if (threadIdx.x == 0) {
         for (int w = 0; w < kWarps; ++w)
@@ -555,65 +567,62 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
-    // All units, then the sequence that holds this CTA's first one.
-    auto units_of = [&](int b, bool report) -> int64_t {
-        if (b >= a.seqs) return 0;
-        const Seq s = seq_of<QC>(a, b, report);
-        return (int64_t)s.units * s.qblocks * a.kv_heads;
+    __syncthreads();  // the barriers are there
+    // The length of the line, then the sequence that holds this CTA's first place: every warp
+    // for itself.
+    auto seq_places = [&](int b, bool report) -> int64_t {
+        return b < a.seqs ? places_of(seq_of<QC>(a, b, report), a.kv_heads) : 0;
     };
-    int64_t sum = 0;
-    for (int b = threadIdx.x; b < a.seqs; b += kWarps * 32) sum += units_of(b, blockIdx.x == 0);
+    const bool report = blockIdx.x == 0 && warp == 0;
+    int64_t mine = seq_places(lane, report), total = mine;
+    for (int b = lane + 32; b < a.seqs; b += 32) total += seq_places(b, report);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sm.sum[warp] = sum;
-    __syncthreads();
-    const int64_t total = sm.sum[0] + sm.sum[1] + sm.sum[2] + sm.sum[3];
-    const int64_t per = share_of(total, ctas);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const int64_t per = share_of(total, gridDim.x);
     const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
+    if (begin >= end && blockIdx.x != 0) return;
+    int b = 0;
+    int64_t seq_first = 0;  // first place of sequence b
     int64_t before = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += kWarps * 32) {
-        const int b = b0 + threadIdx.x;
-        const int64_t mine = units_of(b, false);
+    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
+        if (b0 > 0) mine = seq_places(b0 + lane, false);
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
-        __syncthreads();
-        if (lane == 31) sm.sum[warp] = incl;
-        __syncthreads();
-        int64_t excl = before + incl - mine;
-        for (int w = 0; w < warp; ++w) excl += sm.sum[w];
-        if (blockIdx.x == 0 && b < a.seqs) a.prefix[b] = excl;
-        if (begin >= excl && begin < excl + mine) {
-            sm.found_seq = b;
-            sm.found = excl;
+        const int64_t excl = before + incl - mine;
+        if (report && b0 + lane < a.seqs) a.prefix[b0 + lane] = excl;
+        const unsigned hit = __ballot_sync(0xffffffffu, begin >= excl && begin < excl + mine);
+        if (hit) {
+            b = b0 + __ffs(hit) - 1;
+            seq_first = __shfl_sync(0xffffffffu, excl, __ffs(hit) - 1);
+            if (!report) break;
         }
-        before += sm.sum[0] + sm.sum[1] + sm.sum[2] + sm.sum[3];
-        if (blockIdx.x != 0 && before > begin) break;  // the same for the whole CTA
+        before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.seqs] = total;
-    __syncthreads();
+    if (report && lane == 0) a.prefix[a.seqs] = total;
     if (begin >= end) return;
 
-    int b = sm.found_seq;
-    int64_t seq_first = sm.found;
     Seq s = seq_of<QC>(a, b, false);
     uint32_t phase = 0u, have = 0u;  // per stage: parity waited for next; records in flight
     bool dead = false;
     Warp<D, NT> st;
 
     for (int64_t u = begin; u < end;) {
-        while (u >= seq_first + (int64_t)s.units * s.qblocks * a.kv_heads) {
-            seq_first += (int64_t)s.units * s.qblocks * a.kv_heads;
+        while (u >= seq_first + places_of(s, a.kv_heads)) {
+            seq_first += places_of(s, a.kv_heads);
             s = seq_of<QC>(a, ++b, false);  // u < total, so a sequence with work follows
         }
         const int64_t in_seq = u - seq_first;
-        const int item = in_seq >> 32 ? (int)(in_seq / s.units) : (int)((uint32_t)in_seq / (uint32_t)s.units);
-        const int64_t item_first = seq_first + (int64_t)item * s.units;
-        const int k0 = (int)(u - item_first);
-        const int k1 = (int)min((int64_t)s.units, end - item_first);
+        const int len = s.units + kItemCost;
+        const int item = in_seq >> 32 ? (int)(in_seq / len) : (int)((uint32_t)in_seq / (uint32_t)len);
+        const int64_t first = seq_first + (int64_t)item * len + kItemCost;  // place of unit 0
+        const int k0 = (int)max(u - first, (int64_t)0);
+        const int k1 = (int)min((int64_t)s.units, end - first);
+        u = first + s.units;
+        if (k1 <= k0) continue;
         const int qb = item / a.kv_heads, h = item - qb * a.kv_heads;
         // every column sees the tokens before this one
         const int safe = s.len - s.n + 1 + a.over_group(qb * QC);
@@ -708,43 +717,39 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         }
         __syncthreads();
         const bool whole = k0 == 0 && k1 == s.units;
-        const int slot = item_first <= begin ? 0 : 1;
-        for (int x = threadIdx.x; x < QC * D / 2; x += kWarps * 32) {
-            const int col = x / (D / 2), n = x % (D / 2);
+        const int slot = first < begin ? 0 : 1;
+        for (int x = threadIdx.x; x < QC * D / 4; x += kWarps * 32) {
+            const int col = x / (D / 4), n = x % (D / 4);
             const int idx = qb * QC + col;
             if (idx >= s.n * a.group) continue;
             float m = sm.m[0][col];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm.m[w][col]);
             float l = 0.f;
-            float2 v = make_float2(0.f, 0.f);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float e = ex2(sm.m[w][col] - m);
-                const float2 o = *reinterpret_cast<const float2*>(&sm.w[w].o[col][2 * n]);
+                const float4 o = *reinterpret_cast<const float4*>(&sm.w[w].o[col][4 * n]);
                 l = fmaf(e, sm.l[w][col], l);
                 v.x = fmaf(e, o.x, v.x);
                 v.y = fmaf(e, o.y, v.y);
+                v.z = fmaf(e, o.z, v.z);
+                v.w = fmaf(e, o.w, v.w);
             }
             if (whole) {
-                const float inv = l == 0.f ? 0.f : __frcp_rn(l);
                 const int i = a.over_group(idx), hq = h * a.group + idx - i * a.group;
-                *reinterpret_cast<uint32_t*>(a.out + (int64_t)(s.q0 + i) * a.out_st +
-                                             (int64_t)hq * a.out_sh + dim_of<D>(n)) =
-                    pack_bf16x2(v.x * inv, v.y * inv);
-                if (n == 0 && a.lse)
-                    a.lse[(int64_t)(s.q0 + i) * a.heads + hq] =
-                        l == 0.f ? -__int_as_float(0x7f800000)
-                                 : (m + log2f(l)) * 0.693147180559945309f;
+                const int64_t row = s.q0 + i;
+                put_row<D>(a.out + row * a.out_st + hq * a.out_sh,
+                           a.lse ? a.lse + row * a.heads + hq : nullptr, n, v, m, l);
             } else {
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * QC + col;
-                *reinterpret_cast<float2*>(a.part + at * D + 2 * n) = v;
+                *reinterpret_cast<float4*>(a.part + at * D + 4 * n) = v;
                 if (n == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is next
         __syncthreads();
-        u = item_first + k1;
     }
     // after a wait that ran out: the copies still in flight must land before the CTA ends
     for (int i = 0; i < S; ++i)
@@ -754,14 +759,14 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
 }
 
 // Rows (query token, head) whose item lies in several CTAs, or has no tokens at all.  D/4 lanes
-// hold a row.  WIDE: a CTA per row, whose 1024/D groups of lanes take the partial sums in turn
+// hold a row.  WIDE: a CTA per row, whose 4096/D groups of lanes take the partial sums in turn
 // and are merged in order; otherwise each group has a row of its own (items that lie in a few
 // CTAs only).
-constexpr int kCombineThreads = 256;
+__host__ __device__ constexpr int combine_threads(bool wide) { return wide ? 1024 : 256; }
 
 template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args a, int ctas) {
-    constexpr int QC = 8 * NT, LN = D / 4, GR = kCombineThreads / LN, U = 4;
+__global__ void __launch_bounds__(combine_threads(WIDE)) kv4_combine_kernel(const Args a, int ctas) {
+    constexpr int QC = 8 * NT, LN = D / 4, GR = combine_threads(WIDE) / LN, U = WIDE ? 2 : 4;
     constexpr int STEP = WIDE ? GR : 1;
     __shared__ float4 so[WIDE ? GR : 1][LN];
     __shared__ float smx[GR], sl[GR];
@@ -796,7 +801,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
         return;
     }
     const int64_t per = share_of(a.prefix[a.seqs], ctas);
-    const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * s.units;
+    const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * (s.units + kItemCost) + kItemCost;
     const int64_t u1 = u0 + s.units - 1;
     const int c0 = u1 >> 32 ? (int)(u0 / per) : (int)((uint32_t)u0 / (uint32_t)per);
     const int c1 = u1 >> 32 ? (int)(u1 / per) : (int)((uint32_t)u1 / (uint32_t)per);
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
             ml[i] = make_float2(-FLT_MAX, 0.f);
             o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (cta <= c1) {
-                const int64_t at = (cta * 2 + (u0 <= cta * per ? 0 : 1)) * QC + col;
+                const int64_t at = (cta * 2 + (u0 < cta * per ? 0 : 1)) * QC + col;
                 ml[i] = __ldcg(a.part_ml + at);
                 o[i] = __ldcg(reinterpret_cast<const float4*>(a.part + at * D) + ln);
             }
@@ -837,11 +842,11 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
         }
         __syncthreads();
         if (gr != 0) return;
-#pragma unroll
+#pragma unroll 4
         for (int k = 1; k < GR; ++k) m = fmaxf(m, smx[k]);
         l = 0.f;
         v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 4
         for (int k = 0; k < GR; ++k) {
             const float e = ex2(smx[k] - m);
             const float4 o = so[k][ln];
@@ -852,11 +857,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv4_combine_kernel(const Args
             v.w = fmaf(e, o.w, v.w);
         }
     }
-    const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln)) = pack_bf16x2(v.x * inv, v.y * inv);
-    *reinterpret_cast<uint32_t*>(out + dim_of<D>(2 * ln + 1)) = pack_bf16x2(v.z * inv, v.w * inv);
-    if (ln == 0 && lse)
-        *lse = l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.693147180559945309f;
+    put_row<D>(out, lse, ln, v, m, l);
 }
 
 int64_t prefix_bytes(int seqs) { return ((int64_t)(seqs + 1) * 8 + 255) / 256 * 256; }
@@ -911,10 +912,10 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     // an item lies in about grid / items CTAs (all of the same length): from 8 on, a CTA per row
     const int64_t rows = (int64_t)c.tokens * c.heads, items = (int64_t)c.seqs * c.kv_heads;
     const bool wide = grid >= 8 * items;
-    const int per_cta = wide ? 1 : kCombineThreads * 4 / D;
+    const int per_cta = wide ? 1 : combine_threads(false) * 4 / D;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows + per_cta - 1) / per_cta));
-    cfg.blockDim = dim3(kCombineThreads);
+    cfg.blockDim = dim3(combine_threads(wide));
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
