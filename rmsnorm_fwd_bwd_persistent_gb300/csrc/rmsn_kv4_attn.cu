@@ -161,6 +161,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 // 2^e for e in [-126, 127], limited to that range
 __device__ __forceinline__ float pow2(int e) {
     return __int_as_float((min(max(e, -126), 127) + 127) << 23);
@@ -236,17 +241,21 @@ struct Warp {
     uint32_t qf[NT][NG][4];             // q as binary16 pairs, column g
     uint32_t qz[NT][NZ][2];             // sums of q per group, three bf16 terms, column g
     float f[NT][2];                     // factor of the code products, log2 units
-    int lim[NT][2];                     // tokens that columns 2t and 2t + 1 see
+    int col0, cols, seen0;              // the item's first column, all columns, tokens column 0 sees
     float o[NT][MT][4];                 // times 2^k
     float m[NT][2], l[NT][2];
     int k;                              // of the lane's group of V dims
+    uint32_t bound_s, bound_z;          // 2^(k - 9) and 2^(k + 14) less one step, bf16 twice
     bool first;                         // no unit seen yet
 
     // Loads the item's query rows and resets the sums.
     __device__ __forceinline__ void begin(const Args& a, const Seq& s, int qb, int h, int lane) {
         const int g = lane >> 2, t = lane & 3;
         first = true;
-        k = -100;  // V below about 2^-100 counts as 0
+        set_k(-100);  // V below about 2^-100 counts as 0
+        col0 = qb * NT * 8;
+        cols = s.n * a.group;
+        seen0 = s.len - s.n + 1;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int col = (qb * NT + nt) * 8 + g;
@@ -316,8 +325,6 @@ struct Warp {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 f[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * c);  // of column 2t + c
-                const int cc = (qb * NT + nt) * 8 + 2 * t + c;
-                lim[nt][c] = cc < s.n * a.group ? s.len - s.n + 1 + a.over_group(cc) : 0;
                 m[nt][c] = l[nt][c] = 0.f;
             }
 #pragma unroll
@@ -327,10 +334,21 @@ struct Warp {
         }
     }
 
+    __device__ __forceinline__ void set_k(int kn) {
+        k = kn;
+        bound_s = (uint32_t)(((k - 9 + 127) << 7) - 1) * 0x10001u;
+        bound_z = (uint32_t)((min(k + 14 + 127, 255) << 7) - 1) * 0x10001u;
+    }
+    // Tokens that column 8 nt + c of the item sees.
+    __device__ __forceinline__ int limit(const Args& a, int c) const {
+        const int cc = col0 + c;
+        return cc < cols ? seen0 + a.over_group(cc) : 0;
+    }
+
     // Scores less the reference (log2 units) of the 16 tokens of one record.  FULL: every
     // column sees all of them.
     template <bool FULL>
-    __device__ __forceinline__ void scores(const uint8_t* rec, int tok0, int lane,
+    __device__ __forceinline__ void scores(const Args& a, const uint8_t* rec, int tok0, int lane,
                                            float (&sc)[NT][4]) {
         const int g = lane >> 2, t = lane & 3;
         uint32_t k0[NG], k1[NG], s0[NG], s1[NG];
@@ -372,16 +390,16 @@ struct Warp {
         for (int j = 0; j < NG; ++j) {
             const uint32_t h0 = k0[j] >> 8, h1 = k1[j] >> 8;
             const uint32_t lo = 0x000f000fu, up = 0x00f000f0u;
-            const float a0 = bf16_lo(s0[j]), a1 = bf16_lo(s1[j]);
+            const float f0 = bf16_lo(s0[j]), f1 = bf16_lo(s1[j]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_f16(d, k0[j] & lo, k1[j] & lo, k0[j] & up, k1[j] & up, qf[nt][j][0], qf[nt][j][1]);
                 mma_f16(d, h0 & lo, h1 & lo, h0 & up, h1 & up, qf[nt][j][2], qf[nt][j][3]);
-                sc[nt][0] = fmaf(a0, d[0], sc[nt][0]);
-                sc[nt][1] = fmaf(a0, d[1], sc[nt][1]);
-                sc[nt][2] = fmaf(a1, d[2], sc[nt][2]);
-                sc[nt][3] = fmaf(a1, d[3], sc[nt][3]);
+                sc[nt][0] = fmaf(f0, d[0], sc[nt][0]);
+                sc[nt][1] = fmaf(f0, d[1], sc[nt][1]);
+                sc[nt][2] = fmaf(f1, d[2], sc[nt][2]);
+                sc[nt][3] = fmaf(f1, d[3], sc[nt][3]);
             }
         }
 #pragma unroll
@@ -389,7 +407,7 @@ struct Warp {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 sc[nt][c] = fmaf(sc[nt][c], f[nt][c & 1], zs[nt][c]);
-                if (!FULL && tok0 + g + 8 * (c >> 1) >= lim[nt][c & 1])
+                if (!FULL && tok0 + g + 8 * (c >> 1) >= limit(a, 8 * nt + 2 * t + (c & 1)))
                     sc[nt][c] = -__int_as_float(0x7f800000);
             }
     }
@@ -422,7 +440,7 @@ struct Warp {
 
     // o += V^T P^T for the 16 tokens of one record.
     template <bool FULL>
-    __device__ __forceinline__ void values(const uint8_t* rec, int tok0, int len, int lane, uint2 va,
+    __device__ __forceinline__ void values(const Args& a, const uint8_t* rec, int tok0, int len, int lane, uint2 va,
                                            uint2 vb, bool odd, const float (&sc)[NT][4]) {
         const int g = lane >> 2, t = lane & 3;
         uint32_t b0[NT], b1[NT];
@@ -463,11 +481,12 @@ struct Warp {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][i], a0, a1, a2, a3, b0[nt], b1[nt]);
         }
-        if (!FULL && __any_sync(0xffffffffu, odd)) not_finite(rec, tok0, len, g);
+        if (!FULL && __any_sync(0xffffffffu, odd)) not_finite(a, rec, tok0, len, g, t);
     }
 
     // The columns that see a token whose V is not finite become NaN in that group's dims.
-    __device__ __forceinline__ void not_finite(const uint8_t* rec, int tok0, int len, int g) {
+    __device__ __forceinline__ void not_finite(const Args& a, const uint8_t* rec, int tok0, int len, int g,
+                                               int t) {
         for (int r = 0; r < kKv4Block && tok0 + r < len; ++r) {
             const uint16_t* p =
                 reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, r, g / (256 / D)));
@@ -476,7 +495,7 @@ struct Warp {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    if (tok0 + r < lim[nt][c])
+                    if (tok0 + r < limit(a, 8 * nt + 2 * t + c))
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
                             o[nt][i][c] = __int_as_float(0x7fffffff);
@@ -487,15 +506,16 @@ struct Warp {
 
     // Adds the 32 tokens of one unit; `have`: bit i is set where record i is there.
     template <bool FULL>
-    __device__ __forceinline__ void unit(const uint8_t* rec, int tok0, int len, int have, int lane) {
+    __device__ __forceinline__ void unit(const Args& a, const uint8_t* rec, int tok0, int len, int have,
+                                         int lane) {
         const uint8_t* rec1 = rec + 20 * D;
         const int t = lane & 3;
         // a record that is not there: no token of it is seen
         const int t0 = FULL || (have & 1) ? tok0 : 0x40000000;
         const int t1 = FULL || (have & 2) ? tok0 + kKv4Block : 0x40000000;
         float sc0[NT][4], sc1[NT][4];
-        scores<FULL>(rec, t0, lane, sc0);
-        scores<FULL>(rec1, t1, lane, sc1);
+        scores<FULL>(a, rec, t0, lane, sc0);
+        scores<FULL>(a, rec1, t1, lane, sc1);
         uint2 v[4] = {scale_words(rec, 2 * t, lane), scale_words(rec, 2 * t + 8, lane),
                       scale_words(rec1, 2 * t, lane), scale_words(rec1, 2 * t + 8, lane)};
         bool odd0 = false, odd1 = false;
@@ -503,28 +523,33 @@ struct Warp {
         keep<FULL>(v[1], t0 + 2 * t + 8, len, odd0);
         keep<FULL>(v[2], t1 + 2 * t, len, odd1);
         keep<FULL>(v[3], t1 + 2 * t + 8, len, odd1);
-        const float nd = fmaxf(fmaxf(need(v[0]), need(v[1])), fmaxf(need(v[2]), need(v[3])));
-        bool up = first || nd >= pow2(k);
+        // s < 2^(k - 9) and |z| < 2^(k + 14), as bf16 numbers two at a time
+        const uint32_t ms = max_u16x2(max_u16x2(v[0].x, v[1].x), max_u16x2(v[2].x, v[3].x));
+        const uint32_t mz = max_u16x2(max_u16x2(v[0].y & 0x7fff7fffu, v[1].y & 0x7fff7fffu),
+                                      max_u16x2(v[2].y & 0x7fff7fffu, v[3].y & 0x7fff7fffu));
+        bool up = first || max_u16x2(ms, bound_s) != bound_s || max_u16x2(mz, bound_z) != bound_z;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c)
                 up |= fmaxf(fmaxf(sc0[nt][c], sc0[nt][c + 2]), fmaxf(sc1[nt][c], sc1[nt][c + 2])) > 8.f;
-        if (__any_sync(0xffffffffu, up)) raise(nd, sc0, sc1);
-        values<FULL>(rec, t0, len, lane, v[0], v[1], odd0, sc0);
-        values<FULL>(rec1, t1, len, lane, v[2], v[3], odd1, sc1);
+        if (__any_sync(0xffffffffu, up)) raise(v, sc0, sc1);
+        values<FULL>(a, rec, t0, len, lane, v[0], v[1], odd0, sc0);
+        values<FULL>(a, rec1, t1, len, lane, v[2], v[3], odd1, sc1);
     }
 
     // Moves the references to the unit's largest scores where they are above them (at the first
     // unit in any case), and 2^k above what V needs; rescales the sums.
-    __device__ __forceinline__ void raise(float nd, float (&sc0)[NT][4], float (&sc1)[NT][4]) {
+    __device__ __forceinline__ void raise(const uint2 (&v4)[4], float (&sc0)[NT][4],
+                                          float (&sc1)[NT][4]) {
+        const float nd = fmaxf(fmaxf(need(v4[0]), need(v4[1])), fmaxf(need(v4[2]), need(v4[3])));
         int kn = nd >= pow2(k) && k < 127 ? min(exponent(nd) + 1, 127) : k;
         if (kn < k) kn = k;  // what is not finite asks for nothing
 #pragma unroll
         for (int o2 = 1; o2 < (D == 64 ? 16 : D == 128 ? 8 : 4); o2 <<= 1)
             kn = max(kn, __shfl_xor_sync(0xffffffffu, kn, o2));
         const float rk = pow2(k - kn);
-        k = kn;
+        set_k(kn);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -679,9 +704,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 have &= ~(3u << (2 * stage));
                 const int tok0 = (k0 + warp + i * kWarps) * kUnit;
                 if (got == 3 && tok0 + kUnit <= safe)
-                    st.template unit<true>(sm.w[warp].ring[stage], tok0, s.len, got, lane);
+                    st.template unit<true>(a, sm.w[warp].ring[stage], tok0, s.len, got, lane);
                 else
-                    st.template unit<false>(sm.w[warp].ring[stage], tok0, s.len, got, lane);
+                    st.template unit<false>(a, sm.w[warp].ring[stage], tok0, s.len, got, lane);
                 __syncwarp();
             }
             const int ahead = i + S;
