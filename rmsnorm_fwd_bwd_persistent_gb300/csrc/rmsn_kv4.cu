@@ -7,6 +7,8 @@
 // (IEEE FP32 operations; s = 0: code 0; a group with a NaN or an infinity gets s = z = NaN, so
 // it reads back as NaN).  The codes are a function of the bf16 values alone.
 // kv4_read_kernel is the inverse: code * s + z, rounded once to bf16.
+#include <algorithm>
+
 #include "rmsn_internal.h"
 #include "rmsn_kv4.cuh"
 #include "rmsn_pipe.cuh"
@@ -89,10 +91,37 @@ __device__ __forceinline__ void quantise16(const Raw8<bf16>& a, const Raw8<bf16>
     scale_min = bad ? 0x7fc07fc0u : sb | (lo << 16);
 }
 
+// Stores the codes of dims [16l, 16l + 16) of token r, and from every second lane its group's
+// scale and minimum, to a record.
+template <int D>
+__device__ __forceinline__ void put16(uint8_t* rec, int r, int l, bool k, const uint32_t (&word)[2],
+                                      uint32_t scale_min) {
+    const int j = l >> 1;
+    if (k) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<uint32_t*>(rec + kv4_k_word(D, r, 2 * l + e)) = word[e];
+        if ((l & 1) == 0) *reinterpret_cast<uint32_t*>(rec + kv4_k_scale(D, r, j)) = scale_min;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int wd = 2 * l + e;
+            *reinterpret_cast<uint32_t*>(rec + kv4_v_unit(D, r, wd / (D / 64)) + 4 * (wd % (D / 64))) =
+                word[e];
+        }
+        if ((l & 1) == 0) {
+            uint16_t* p = reinterpret_cast<uint16_t*>(rec + kv4_v_scale(D, r, j));
+            p[0] = (uint16_t)(scale_min & 0xffffu);
+            p[2] = (uint16_t)(scale_min >> 16);
+        }
+    }
+}
+
 struct AppendArgs {
     Heads x[3], y;  // q, k, v in; q out
     const void* w[2];
     Span span[3];
+    int grid[3];  // CTAs of q, k and v (streaming kernel)
     Rope rope;
     uint8_t* cache;
     const int64_t* slots;
@@ -207,29 +236,255 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
             uint32_t word[2], sm;
             quantise16(r0[i], r1[i], word, sm);
             if (!row_ok) continue;
-            uint8_t* rec = rec0 + h * head_bytes;
-            const int j = l >> 1;
-            if (side == 1) {
+            put16<D>(rec0 + h * head_bytes, r, l, side == 1, word, sm);
+        }
+    }
+}
+
+// rotate() on pairs.  (Half pairs: the lane's vectors are the partners, two at a time;
+// neighbours: one at a time.)
+template <bool NEIGHBOURS, bool TRANSPOSE>
+__device__ __forceinline__ void rotate2(f2 (&u)[4], f2 (&v)[4], const Angles& t) {
+    if constexpr (NEIGHBOURS) {
+        float a[8], b[8];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<uint32_t*>(rec + kv4_k_word(D, r, 2 * l + e)) = word[e];
-                if ((l & 1) == 0)
-                    *reinterpret_cast<uint32_t*>(rec + kv4_k_scale(D, r, j)) = sm;
+        for (int i = 0; i < 4; ++i) {
+            a[2 * i] = f2_lo(u[i]);
+            a[2 * i + 1] = f2_hi(u[i]);
+            b[2 * i] = f2_lo(v[i]);
+            b[2 * i + 1] = f2_hi(v[i]);
+        }
+        rotate<true, TRANSPOSE>(a, b, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = f2_make(a[2 * i], a[2 * i + 1]);
+            v[i] = f2_make(b[2 * i], b[2 * i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f2 c = f2_make(t.c[2 * i], t.c[2 * i + 1]);
+            const f2 s = f2_make(t.s[2 * i], t.s[2 * i + 1]);
+            const f2 x = u[i], y = v[i];
+            if (TRANSPOSE) {
+                u[i] = fma2(y, s, mul2(x, c));
+                v[i] = sub2(mul2(y, c), mul2(x, s));
             } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int wd = 2 * l + e;
-                    *reinterpret_cast<uint32_t*>(rec + kv4_v_unit(D, r, wd / (D / 64)) +
-                                                 4 * (wd % (D / 64))) = word[e];
-                }
-                if ((l & 1) == 0) {
-                    uint16_t* p = reinterpret_cast<uint16_t*>(rec + kv4_v_scale(D, r, j));
-                    p[0] = (uint16_t)(sm & 0xffffu);
-                    p[2] = (uint16_t)(sm >> 16);
-                }
+                u[i] = sub2(mul2(x, c), mul2(y, s));
+                v[i] = fma2(x, s, mul2(y, c));
             }
         }
     }
+}
+
+// (x r) w, rotated: the forward of one row's lane.
+template <bool NEIGHBOURS, int LPR>
+__device__ __forceinline__ void norm_rotate(f2 (&u)[4], f2 (&v)[4], const f2 (&w0)[4], const f2 (&w1)[4],
+                                            const Angles& ang, float inv_d, float eps) {
+    f2 ss2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss2 = fma2(u[i], u[i], ss2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss2 = fma2(v[i], v[i], ss2);
+    const float r = row_rstd(row_sum<LPR>(f2_lo(ss2) + f2_hi(ss2)), inv_d, eps);
+    const f2 r2 = f2_splat(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u[i] = mul2(mul2(u[i], r2), w0[i]);
+        v[i] = mul2(mul2(v[i], r2), w1[i]);
+    }
+    rotate2<NEIGHBOURS, false>(u, v, ang);
+}
+
+// The weights beside a lane's two vectors (zero where it has none).
+__device__ __forceinline__ void load_weights(const void* w, int bf16, int off0, int off1, bool ok,
+                                             f2 (&w0)[4], f2 (&w1)[4]) {
+    float f0[8], f1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f0[i] = f1[i] = 0.f;
+    if (ok) {
+        load_w8(w, bf16, off0, f0);
+        load_w8(w, bf16, off1, f1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w0[i] = f2_make(f0[2 * i], f0[2 * i + 1]);
+        w1[i] = f2_make(f1[2 * i], f1[2 * i + 1]);
+    }
+}
+
+// A warp's place in its line of units: the unit, the chunks [c, c1) of its part of the heads, and
+// the token of this lane's row (tokens where there is none).
+struct UnitAt {
+    int64_t unit;
+    int c, c1, tok;
+
+    __device__ __forceinline__ void enter(const Span& sp, int tpw, int tsub, int tokens) {
+        const int64_t grp = sp.parts == 1 ? unit
+                            : (unit >> 32) ? unit / sp.parts
+                                           : (int64_t)((uint32_t)unit / (uint32_t)sp.parts);
+        const int part = (int)(unit - grp * sp.parts);
+        c = part * sp.per_part;
+        c1 = min(sp.chunks, c + sp.per_part);
+        tok = (int)min(grp * tpw + tsub, (int64_t)tokens);
+    }
+};
+
+// A tensor's rows streamed through a ring in shared memory that belongs to the lane alone: S
+// stages of one chunk, copied asynchronously S - 1 chunks ahead (across units too), so the bytes
+// in flight cost neither registers nor barriers.  Rows that do not exist are not copied; what
+// their places hold is not used.
+template <int S>
+struct RowStream {
+    using Ring = uint4[S][2][32];  // of one warp
+
+    const bf16 *p0, *p1;
+    int64_t step, stride, units;
+    UnitAt in;
+    uint32_t ring;
+    int hsub, tsub, tpw;
+
+    __device__ __forceinline__ void rows(const Heads& x, const Span& sp, int off0, int off1, int tokens) {
+        if (in.unit >= units) return;
+        in.enter(sp, tpw, tsub, tokens);
+        const bf16* row = x.row<bf16>(0, in.tok < tokens ? in.tok : 0) + ((in.c << sp.log_hpw) + hsub) * x.sh;
+        p0 = row + off0;
+        p1 = row + off1;
+    }
+
+    // Copies the next chunk, if there is one, to a stage.
+    __device__ __forceinline__ void fetch(int stage, const Heads& x, const Span& sp, int off0, int off1,
+                                          int tokens) {
+        if (in.unit < units) {
+            if (in.tok < tokens && (in.c << sp.log_hpw) + hsub < sp.heads) {
+                copy16(ring + (uint32_t)stage * 1024, p0);
+                copy16(ring + (uint32_t)stage * 1024 + 512, p1);
+            }
+            p0 += step;
+            p1 += step;
+            if (++in.c == in.c1) {
+                in.unit += stride;
+                rows(x, sp, off0, off1, tokens);
+            }
+        }
+        copy_commit();
+    }
+};
+
+constexpr int kAppendStages = 6;  // 6 KiB per warp
+constexpr int kStreamFrom = 4;    // units per warp from which the streaming kernel is taken
+
+struct AppendSmem {
+    RowStream<kAppendStages>::Ring ring[kWarps];
+    bf16 turn[kWarps][512];  // rows of k on their way to neighbouring dims
+};
+
+// The same for many tokens: persistent, with CTAs for q, for k and for v, each warp streaming the
+// rows of its units.  Measured with 32 + 8 + 8 heads of 128: at 16384 tokens (with the read that
+// follows) 111.5 us with the kernel above, 97.8 so; at 64 tokens, where there is nothing to run
+// ahead of, 7.6 and 8.5.
+template <int LPR, bool NB>
+__global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const AppendArgs a) {
+    constexpr int RPW = 32 / LPR, D = 16 * LPR, S = kAppendStages;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    auto& sm = *reinterpret_cast<AppendSmem*>(smem_raw);
+    int side = 0, cta = blockIdx.x;
+    while (side < 2 && cta >= a.grid[side]) cta -= a.grid[side++];
+    const Span sp = a.span[side];
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, l = lane % LPR, rr = lane / LPR;
+    const int hsub = rr & ((1 << sp.log_hpw) - 1), tsub = rr >> sp.log_hpw;
+    const int tpw = RPW >> sp.log_hpw;
+    const int64_t units = ((int64_t)a.tokens + tpw - 1) / tpw * sp.parts;
+    const int64_t first = (int64_t)cta * kWarps + warp, stride = (int64_t)a.grid[side] * kWarps;
+    RowLane<NB> rl;
+    rl.init(l, side == 2 ? 0 : a.rope.rd);
+    const Heads& x = a.x[side];
+    RowStream<S> rows;
+    rows.ring = smem_addr(&sm.ring[warp][0][0][lane]);
+    rows.stride = stride;
+    rows.units = units;
+    rows.hsub = hsub;
+    rows.tsub = tsub;
+    rows.tpw = tpw;
+    rows.step = (int64_t)(1 << sp.log_hpw) * x.sh;
+    rows.in.unit = first;
+    rows.rows(x, sp, rl.off0, rl.off1, a.tokens);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) rows.fetch(i, x, sp, rl.off0, rl.off1, a.tokens);
+    f2 w0[4], w1[4];
+    load_weights(a.w[side & 1], a.w_bf16, rl.off0, rl.off1, side < 2, w0, w1);
+    const int hpw = 1 << sp.log_hpw;
+    const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
+    int stage = 0;
+    for (UnitAt at{first, 0, 0, 0}; at.unit < units; at.unit += stride) {
+        at.enter(sp, tpw, tsub, a.tokens);
+        const Token tk = find_token(at.tok, a.tokens, a.tokens, a.rope, a.err, false);
+        bool ok = false;
+        int r = 0;  // the token's place in its record
+        bf16* y = a.y.row<bf16>(0, tk.t);
+        uint8_t* rec = a.cache;
+        if (at.tok < a.tokens) {
+            const int64_t slot = __ldg(a.slots + tk.t);
+            const bool in = slot < a.pages * a.blocks_per_page * kKv4Block;
+            ok = tk.ok && slot >= 0 && in;
+            if (slot >= 0 && (!in || !tk.ok) && side == 0 && at.c == 0 && l == 0 && hsub == 0)
+                atomicOr(a.err, ERR_INDEX);
+            if (ok && side > 0) {
+                rec += kv4_record_of(slot, a.blocks_per_page, a.kv_heads) * kv4_record_bytes(D);
+                r = (int)(slot & (kKv4Block - 1));
+            }
+        }
+        Angles ang;
+        ang.identity();
+        if (ok && rl.turns) {
+            const int64_t p = tk.pos * (a.rope.rd / 2) + 8 * l;
+            ang.load(a.rope.cos + p, a.rope.sin + p);
+        }
+        int h = (at.c << sp.log_hpw) + hsub;
+        y += h * a.y.sh;
+        rec += h * head_bytes;
+        for (int c = at.c; c < at.c1; ++c) {
+            copy_wait<S - 2>();
+            const uint4* slot = &sm.ring[warp][stage][0][lane];
+            Raw8<bf16> r0{slot[0]}, r1{slot[32]};
+            // the stage read one chunk ago is free: every lane reads its own
+            rows.fetch(stage == 0 ? S - 1 : stage - 1, x, sp, rl.off0, rl.off1, a.tokens);
+            stage = stage + 1 == S ? 0 : stage + 1;
+            const bool row_ok = ok && h < sp.heads;
+            if (side < 2) {
+                f2 u[4], v[4];
+                Pairs<bf16>::get(r0.a, u);
+                Pairs<bf16>::get(r1.a, v);
+                norm_rotate<NB, LPR>(u, v, w0, w1, ang, 1.f / D, a.eps);
+                r0.a = Pairs<bf16>::put(u);
+                r1.a = Pairs<bf16>::put(v);
+            }
+            if (side == 0) {
+                if (row_ok) {
+                    r0.store(y + rl.off0);
+                    r1.store(y + rl.off1);
+                }
+            } else {
+                if (!NB && side == 1) {  // to neighbouring dims: lane l takes dims [16l, 16l + 16)
+                    bf16* row = sm.turn[warp] + rr * D;
+                    r0.store(row + rl.off0);
+                    r1.store(row + rl.off1);
+                    __syncwarp();
+                    r0.a = *reinterpret_cast<const uint4*>(row + 16 * l);
+                    r1.a = *reinterpret_cast<const uint4*>(row + 16 * l + 8);
+                    __syncwarp();
+                }
+                uint32_t word[2], sz;
+                quantise16(r0, r1, word, sz);
+                if (row_ok) put16<D>(rec, r, l, side == 1, word, sz);
+            }
+            h += hpw;
+            y += hpw * a.y.sh;
+            rec += hpw * head_bytes;
+        }
+    }
+    copy_wait<0>();
 }
 
 __device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
@@ -330,19 +585,38 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
     }
 }
 
+// Shares `all` CTAs of `warps` warps out to `sides` tensors by their work: a unit's chunks, and
+// `enter` chunks' time for entering it, times the tensor's own factor.
+void share_ctas(int64_t all, int warps, int sides, const Span* sp, const int64_t* units,
+                       const double* factor, double enter, int* grid) {
+    double work[3] = {0, 0, 0}, sum = 0;
+    for (int i = 0; i < sides; ++i) {
+        work[i] = (double)units[i] * (sp[i].per_part * factor[i] + enter);
+        sum += work[i];
+    }
+    for (int i = 0; i < sides; ++i) {
+        int64_t g = (int64_t)((double)all * work[i] / sum + 0.5);
+        const int64_t need = (units[i] + warps - 1) / warps;
+        g = g < 1 ? 1 : g;
+        grid[i] = (int)(need < g ? need : g);
+    }
+}
+
 template <int LPR, bool NB>
 cudaError_t run_append(const Kv4Append& c, cudaStream_t s) {
     constexpr int RPW = 32 / LPR;
     AppendArgs a{};
     const int heads[3] = {c.heads, c.kv_heads, c.kv_heads};
     const int per = pick_per_part(heads, 3, c.tokens, RPW, c.sms);
-    int64_t gx = 1;
+    int64_t units[3], gx = 1, sum = 0;
     int gy = 0;
     for (int i = 0; i < 3; ++i) {
         a.x[i] = c.x[i];
         a.span[i] = make_span(heads[i], RPW, per);
-        const int64_t g = (groups_of(c.tokens, a.span[i], RPW) + kWarps - 1) / kWarps;
-        gx = g > gx ? g : gx;
+        const int64_t g = groups_of(c.tokens, a.span[i], RPW);
+        units[i] = g * a.span[i].parts;
+        sum += units[i];
+        gx = std::max(gx, (g + kWarps - 1) / kWarps);
         gy += a.span[i].parts;
     }
     a.y = c.y;
@@ -358,7 +632,22 @@ cudaError_t run_append(const Kv4Append& c, cudaStream_t s) {
     a.kv_heads = c.kv_heads;
     a.w_bf16 = c.w_dt;
     a.eps = c.eps;
-    kv4_append_kernel<LPR, NB><<<dim3((unsigned)gx, gy), kWarps * 32, 0, s>>>(a);
+    if (sum < (int64_t)c.sms * 16 * kStreamFrom) {  // 16 warps run on an SM at once
+        kv4_append_kernel<LPR, NB><<<dim3((unsigned)gx, gy), kWarps * 32, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    Launch L{};
+    L.sms = c.sms;
+    L.grid = (int64_t)c.sms * 16;
+    L.smem = sizeof(AppendSmem);
+    int64_t all = 0;
+    auto kernel = kv4_append_stream_kernel<LPR, NB>;
+    cudaError_t e = fit_grid((const void*)kernel, L, kWarps * 32, &all);
+    if (e != cudaSuccess) return e;
+    // norm and rotation, both and the quantiser, the quantiser alone
+    const double factor[3] = {1, 1.8, 1.2};
+    share_ctas(all, kWarps, 3, a.span, units, factor, 1.5, a.grid);
+    kernel<<<a.grid[0] + a.grid[1] + a.grid[2], kWarps * 32, (size_t)L.smem, s>>>(a);
     return cudaGetLastError();
 }
 

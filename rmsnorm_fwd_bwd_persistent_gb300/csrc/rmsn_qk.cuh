@@ -234,6 +234,39 @@ inline int pick_per_part(const int* heads, int sides, int64_t tokens, int rpw, i
     return per;
 }
 
+// 16 bytes from global to this lane's own place in shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Eight elements at a lane's place in its ring, as FP32 pairs, and back to memory.
+template <typename T>
+__device__ __forceinline__ void pairs8(const uint4* p, f2 (&f)[4]) {
+    if constexpr (sizeof(T) == 2) {
+        Pairs<__nv_bfloat16>::get(p[0], f);
+    } else {
+        const uint4 a = p[0], b = p[32];
+        f[0] = f2_make(__uint_as_float(a.x), __uint_as_float(a.y));
+        f[1] = f2_make(__uint_as_float(a.z), __uint_as_float(a.w));
+        f[2] = f2_make(__uint_as_float(b.x), __uint_as_float(b.y));
+        f[3] = f2_make(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const f2 (&f)[4]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = Pairs<__nv_bfloat16>::put(f);
+    } else {
+        reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
+        reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
+    }
+}
+
 // A checked call of the norm + rotation (x -> y, or with ws the backward: g, x -> y = dx).
 struct QkCall {
     Heads x[2], y[2], g[2];
