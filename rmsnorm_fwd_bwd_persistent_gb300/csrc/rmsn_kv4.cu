@@ -487,10 +487,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const Ap
     copy_wait<0>();
 }
 
-__device__ __forceinline__ uint32_t ldg_word(const uint8_t* p) {
-    return __ldg(reinterpret_cast<const uint32_t*>(p));
-}
-
 // Eight codes -> eight bf16 values c s + z, one rounding each (s and z twice in their words).
 // 128 + c is a bf16 with the code in its low bits, so c comes out exactly; the FMA rounds.
 __device__ __forceinline__ uint4 values8(uint32_t word, uint32_t s2, uint32_t z2) {
@@ -512,76 +508,97 @@ struct ReadArgs {
     Span span;
     int64_t pages;
     unsigned* err;
-    int tokens, blocks_per_page, log_cpt;
+    int tokens, blocks_per_page;
+    bool wide;  // 32-byte stores: every row of k and v starts on 32 bytes
 };
 
-// A warp takes U steps of rows at a time: `cpt` chunks of heads (1, 2 or 4) of U / cpt token
-// groups, so as many loads are in flight whatever the number of heads.  Lane l of a row takes the
-// dims 8l .. 8l + 7 of each half of the head, so that a store of the warp writes whole rows.
-constexpr int kReadSteps = 4;
+// 16 neighbouring dims to memory.
+__device__ __forceinline__ void store16(bf16* p, const uint4& a, const uint4& b, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+                     "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = a;
+        reinterpret_cast<uint4*>(p)[1] = b;
+    }
+}
 
-template <int LPR>
+// Lanes per row D/64: a lane takes 64 dims of K and 64 of V, which are 32 bytes of codes each (K:
+// the 16 dims 16 h .. of four groups, two words each; V: neighbours), so it loads six 16-byte
+// pieces and writes eight of 32 bytes, whole sectors.  Measured at 32768 tokens of 8 heads of 128
+// (floor 26 us): 42 us with 16 dims per lane, ten loads of 2 to 4 bytes and four times the lanes'
+// instructions.
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a) {
-    constexpr int RPW = 32 / LPR, D = 16 * LPR, U = kReadSteps;
+    constexpr int LN = D / 64, RPW = 32 / LN;
     const Span sp = a.span;
     const int part = blockIdx.y;
-    const int lane = threadIdx.x & 31, l = lane % LPR, rr = lane / LPR;
+    const int lane = threadIdx.x & 31, q = lane % LN, rr = lane / LN;
     const int hsub = rr & ((1 << sp.log_hpw) - 1), tsub = rr >> sp.log_hpw;
     const int tpw = RPW >> sp.log_hpw;
-    const int64_t first =
-        ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * (U >> a.log_cpt) * tpw + tsub;
-    const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
-    const uint8_t* rec0[U];  // the record of head 0; null: nothing to do
-    int row[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t tok = first + (i >> a.log_cpt) * tpw;
-        const int64_t slot = tok < a.tokens ? __ldg(a.slots + tok) : -1;
-        rec0[i] = nullptr;
-        row[i] = (int)(slot & (kKv4Block - 1));
-        if (slot >= a.pages * a.blocks_per_page * kKv4Block) {
-            if (part == 0 && l == 0 && hsub == 0) atomicOr(a.err, ERR_INDEX);
-        } else if (slot >= 0) {
-            rec0[i] = a.cache + kv4_record_of(slot, a.blocks_per_page, sp.heads) *
-                                    kv4_record_bytes(D);
-        }
+    const int64_t tok = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * tpw + tsub;
+    if (tok >= a.tokens) return;
+    const int64_t slot = __ldg(a.slots + tok);
+    if (slot < 0) return;
+    if (slot >= a.pages * a.blocks_per_page * kKv4Block) {
+        if (part == 0 && q == 0 && hsub == 0) atomicOr(a.err, ERR_INDEX);
+        return;
     }
-    const int c1 = min(sp.chunks, (part + 1) * sp.per_part);
-    for (int c0 = part * sp.per_part; c0 < c1; c0 += 1 << a.log_cpt) {
-        uint32_t kw[U][2], vw[U][2], ks[U][2], vs[U][2];
-        bool ok[U];
+    const int r = (int)(slot & (kKv4Block - 1));
+    const int h16 = q & 1, quad = q >> 1;  // K: dims 16 h16 .. of groups 4 quad ..  (D = 64: both h16)
+    const int64_t head_bytes = (int64_t)a.blocks_per_page * kv4_record_bytes(D);
+    int h = (part * sp.per_part << sp.log_hpw) + hsub;
+    const uint8_t* rec = a.cache + kv4_record_of(slot, a.blocks_per_page, sp.heads) * kv4_record_bytes(D) +
+                         h * head_bytes;
+    bf16* ko = a.k.row<bf16>(0, (int)tok) + h * a.k.sh;
+    bf16* vo = a.v.row<bf16>(0, (int)tok) + h * a.v.sh + 64 * q;
+    const int h1 = min(sp.heads, (part + 1) * sp.per_part << sp.log_hpw), hpw = 1 << sp.log_hpw;
+    // byte offsets of the lane's pieces in a record
+    const int k0 = D == 64 ? kv4_k_word(D, r, 0) : kv4_k_word(D, r, 2 * h16 + 16 * quad);
+    const int k1 = D == 64 ? k0 + 16 : kv4_k_word(D, r, 2 * h16 + 1 + 16 * quad);
+    const int ks = kv4_k_scale(D, r, 4 * quad);
+    const int v0 = kv4_v_unit(D, r, 8 / LN * q), vs = kv4_v_scale(D, r & ~1, 2 * q);
+    const uint32_t odd = r & 1 ? 0x3232 : 0x1010;  // this token's half of a pair of scales
+    for (; h < h1; h += hpw) {
+        uint32_t kw[8], vw[8], sk[4], sv[4];
+        auto load4 = [&](int at, uint32_t* w) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + at));
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
+        };
+        load4(k0, kw);
+        load4(k1, kw + 4);
+        if (D == 64) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(rec + ks));
+            sk[0] = x.x;
+            sk[1] = x.y;
+        } else {
+            load4(ks, sk);
+        }
+        load4(v0, vw);
+        load4(v0 + 16, vw + 4);
+        load4(vs, sv);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int c = c0 + (i & ((1 << a.log_cpt) - 1));
-            const int h = (c << sp.log_hpw) + hsub;
-            ok[i] = rec0[i] && c < c1 && h < sp.heads;
-            if (!ok[i]) continue;
-            const uint8_t* rec = rec0[i] + h * head_bytes;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int wd = l + LPR * e, j = wd >> 2;
-                kw[i][e] = ldg_word(rec + kv4_k_word(D, row[i], wd));
-                vw[i][e] = ldg_word(rec + kv4_v_unit(D, row[i], wd / (D / 64)) + 4 * (wd % (D / 64)));
-                ks[i][e] = ldg_word(rec + kv4_k_scale(D, row[i], j));
-                const uint16_t* p = reinterpret_cast<const uint16_t*>(rec + kv4_v_scale(D, row[i], j));
-                vs[i][e] = __byte_perm(__ldg(p), __ldg(p + 2), 0x5410);
-            }
+        for (int i = 0; i < 4; ++i) {
+            // D = 64: words (t, j) at 2 t + j; else t = 2 h16 in kw[0 .. 3], 2 h16 + 1 in kw[4 .. 7]
+            const int j = D == 64 ? i / 2 : i, half = D == 64 ? i % 2 : h16;
+            const uint32_t wa = D == 64 ? kw[4 * (i % 2) + j] : kw[i];
+            const uint32_t wb = D == 64 ? kw[4 * (i % 2) + 2 + j] : kw[4 + i];
+            const uint32_t s2 = __byte_perm(sk[j], 0, 0x1010), z2 = __byte_perm(sk[j], 0, 0x3232);
+            store16(ko + 32 * (4 * quad + j) + 16 * half, values8(wa, s2, z2), values8(wb, s2, z2), a.wide);
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (!ok[i]) continue;
-            const int h = ((c0 + (i & ((1 << a.log_cpt) - 1))) << sp.log_hpw) + hsub;
-            const int tok = (int)(first + (i >> a.log_cpt) * tpw);
-            bf16* ko = a.k.row<bf16>(0, tok) + h * a.k.sh + 8 * l;
-            bf16* vo = a.v.row<bf16>(0, tok) + h * a.v.sh + 8 * l;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                st_stream(ko + D / 2 * e, values8(kw[i][e], __byte_perm(ks[i][e], 0, 0x1010),
-                                                  __byte_perm(ks[i][e], 0, 0x3232)));
-                st_stream(vo + D / 2 * e, values8(vw[i][e], __byte_perm(vs[i][e], 0, 0x1010),
-                                                  __byte_perm(vs[i][e], 0, 0x3232)));
-            }
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t s2 = __byte_perm(sv[2 * (i / 2)], 0, odd);
+            const uint32_t z2 = __byte_perm(sv[2 * (i / 2) + 1], 0, odd);
+            store16(vo + 16 * i, values8(vw[2 * i], s2, z2), values8(vw[2 * i + 1], s2, z2), a.wide);
         }
+        rec += hpw * head_bytes;
+        ko += hpw * a.k.sh;
+        vo += hpw * a.v.sh;
     }
 }
 
@@ -651,9 +668,9 @@ cudaError_t run_append(const Kv4Append& c, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int LPR>
+template <int D>
 cudaError_t run_read(const Kv4Read& c, cudaStream_t s) {
-    constexpr int RPW = 32 / LPR;
+    constexpr int RPW = 32 * 64 / D;
     ReadArgs a{};
     const int per = pick_per_part(&c.kv_heads, 1, c.tokens, RPW, c.sms);
     a.cache = c.cache;
@@ -665,10 +682,12 @@ cudaError_t run_read(const Kv4Read& c, cudaStream_t s) {
     a.err = c.err;
     a.tokens = (int)c.tokens;
     a.blocks_per_page = c.blocks_per_page;
-    while (a.log_cpt < 2 && (2 << a.log_cpt) <= a.span.per_part) ++a.log_cpt;
-    const int64_t per_cta = (int64_t)kWarps * (kReadSteps >> a.log_cpt);
-    const int64_t gx = (groups_of(c.tokens, a.span, RPW) + per_cta - 1) / per_cta;
-    kv4_read_kernel<LPR><<<dim3((unsigned)gx, a.span.parts), kWarps * 32, 0, s>>>(a);
+    a.wide = true;
+    for (const Heads* x : {&c.k, &c.v})
+        if ((reinterpret_cast<uintptr_t>(x->p) | (uintptr_t)x->st * 2 | (uintptr_t)x->sh * 2) % 32 != 0)
+            a.wide = false;
+    const int64_t gx = (groups_of(c.tokens, a.span, RPW) + kWarps - 1) / kWarps;
+    kv4_read_kernel<D><<<dim3((unsigned)gx, a.span.parts), kWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -685,9 +704,9 @@ cudaError_t launch_kv4_append(const Kv4Append& c, cudaStream_t s) {
 
 cudaError_t launch_kv4_read(const Kv4Read& c, cudaStream_t s) {
     switch (c.D) {
-        case 64: return run_read<4>(c, s);
-        case 128: return run_read<8>(c, s);
-        case 256: return run_read<16>(c, s);
+        case 64: return run_read<64>(c, s);
+        case 128: return run_read<128>(c, s);
+        case 256: return run_read<256>(c, s);
         default: return cudaErrorInvalidValue;
     }
 }

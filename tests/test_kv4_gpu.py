@@ -70,6 +70,23 @@ def test_append_and_read(T, Hq, Hk, D, rd, ps, nb):
     assert rmsn.rmsn_device_status() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_read_into_strided_rows(D):
+    """Rows that start on 16 bytes but not on 32, and rows with gaps: the same values, the gaps untouched."""
+    cache, table, g = filled([40], 3, 16, D, seed=D)
+    slots = torch.cat([table[0, :3].long()[torch.arange(40) // 16] * 16 + torch.arange(40) % 16, torch.tensor([-1])])
+    k, v = rmsn.kv4_read(cache.to(DEV), slots.to(DEV), *(torch.zeros(41, 3, D, dtype=BF16, device=DEV) for _ in "kv"))
+    for off, gap in ((8, 0), (0, 8), (16, 16)):
+        buf = torch.full((2, 41 * 3 * (D + gap) + 32), 7.0, dtype=BF16, device=DEV)
+        ko, vo = (b[off:off + 41 * 3 * (D + gap)].view(41, 3, D + gap)[..., :D] for b in buf)
+        rmsn.kv4_read(cache.to(DEV), slots.to(DEV), ko, vo)
+        assert torch.equal(ko[:40], k[:40]) and torch.equal(vo[:40], v[:40])
+        ko[:40] = 7
+        vo[:40] = 7
+        assert (buf == 7).all()
+    assert rmsn.rmsn_device_status() == 0
+
+
 def test_append_in_place_and_overwriting():
     T, Hq, Hk, D = 24, 4, 2, 128
     cache = empty_cache(3, Hk, 16, D)
