@@ -512,18 +512,6 @@ struct ReadArgs {
     bool wide;  // 32-byte stores: every row of k and v starts on 32 bytes
 };
 
-// 16 neighbouring dims to memory.
-__device__ __forceinline__ void store16(bf16* p, const uint4& a, const uint4& b, bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
-                     "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(p)[0] = a;
-        reinterpret_cast<uint4*>(p)[1] = b;
-    }
-}
-
 // Lanes per row D/64: a lane takes 64 dims of K and 64 of V, which are 32 bytes of codes each (K:
 // the 16 dims 16 h .. of four groups, two words each; V: neighbours), so it loads six 16-byte
 // pieces and writes eight of 32 bytes, whole sectors.  Measured at 32768 tokens of 8 heads of 128
@@ -588,13 +576,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
             const uint32_t wa = D == 64 ? kw[4 * (i % 2) + j] : kw[i];
             const uint32_t wb = D == 64 ? kw[4 * (i % 2) + 2 + j] : kw[4 + i];
             const uint32_t s2 = __byte_perm(sk[j], 0, 0x1010), z2 = __byte_perm(sk[j], 0, 0x3232);
-            store16(ko + 32 * (4 * quad + j) + 16 * half, values8(wa, s2, z2), values8(wb, s2, z2), a.wide);
+            store32(ko + 32 * (4 * quad + j) + 16 * half, values8(wa, s2, z2), values8(wb, s2, z2), a.wide);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t s2 = __byte_perm(sv[2 * (i / 2)], 0, odd);
             const uint32_t z2 = __byte_perm(sv[2 * (i / 2) + 1], 0, odd);
-            store16(vo + 16 * i, values8(vw[2 * i], s2, z2), values8(vw[2 * i + 1], s2, z2), a.wide);
+            store32(vo + 16 * i, values8(vw[2 * i], s2, z2), values8(vw[2 * i + 1], s2, z2), a.wide);
         }
         rec += hpw * head_bytes;
         ko += hpw * a.k.sh;

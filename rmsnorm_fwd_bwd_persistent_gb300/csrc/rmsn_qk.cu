@@ -31,6 +31,7 @@ struct FwdArgs {
     Rope rope;
     unsigned* err;
     int tokens, T, D, w_bf16;
+    bool wide;  // rows of the outputs start on 32 bytes
     float eps;
 };
 
@@ -109,11 +110,15 @@ __global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
                 v[e] = v[e] * r * w1[e];
             }
             rotate<NB, false>(u, v, ang);
-            r0[i].set(u);
-            r1[i].set(v);
             if (lane_ok && h < sp.heads) {
-                r0[i].store(y + h * syh + rl.off0);
-                r1[i].store(y + h * syh + rl.off1);
+                f2 y0[4], y1[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y0[e] = f2_make(u[2 * e], u[2 * e + 1]);
+                    y1[e] = f2_make(v[2 * e], v[2 * e + 1]);
+                }
+                T* to = y + h * syh;
+                store_row<T, NB>(to + rl.off0, to + rl.off1, y0, y1, a.wide);
             }
         }
     }
@@ -128,18 +133,17 @@ struct BwdArgs {
     float* ws;    // [CTA][hi, lo][D]
     unsigned* err;
     int tokens, T, D, w_bf16;
+    bool wide;  // rows of the outputs start on 32 bytes
     float eps;
 };
 
-// Shared memory of the backward: every lane's ring of its own 16-byte pieces (x and g of one
-// chunk per stage), and its (high, low) sums.
+// Shared memory of the backward: the rings of rows of x and g, as they lie in memory (a row of
+// LPR lanes has LPR * 16 elements' room), and every lane's (high, low) sums.
 template <typename T>
 struct BwdSmem {
-    static constexpr int V = sizeof(T) / 2;  // pieces per vector of 8 elements
-    static constexpr int NV = 4 * V;         // pieces per stage: two vectors of x, two of g
     static constexpr int S = sizeof(T) == 2 ? 5 : 3;  // 10 and 12 KiB per warp
     union {
-        uint4 ring[kWarps][S][NV][32];
+        T ring[kWarps][S][2][512];
         float merge[kWarps][2][256];
     };
     ulonglong2 sums[2][4][kWarps * 32];  // high, low: four pairs of f2 per lane
@@ -147,8 +151,10 @@ struct BwdSmem {
 
 // Persistent: the first grid[0] CTAs take q's units, the others k's; a unit is tpw tokens and
 // one part of their heads (up to 8 chunks).  Rows stream through a ring in shared memory that
-// belongs to the lane alone (asynchronous copies, no barriers), so the bytes in flight do not
-// cost registers.  A lane adds the dw terms of up to kBlock chunks in FP32 and such sums to
+// belongs to the warp (asynchronous copies, no CTA barriers), so the bytes in flight do not cost
+// registers.  The lanes of a row copy it piece by piece in the order of memory, whatever dims they
+// work on: with each lane copying its own dims, 16-byte pieces 32 bytes apart (FP32; neighbouring
+// pairs) held the copies to 2.8 TB/s at any depth of the ring (FP32, T = 8192: 121 us).  A lane adds the dw terms of up to kBlock chunks in FP32 and such sums to
 // a (high, low) pair with TwoSum; the pairs of the CTA's lanes are merged in a fixed order and
 // written to the workspace, whose CTA partials qk_dw_reduce_kernel adds in a fixed order.
 // Two-element FP32 instructions halve the arithmetic.  Measured on GB300 at T = 32768, 32 + 8
@@ -157,7 +163,7 @@ template <typename T, int LPR, bool NB>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
     qk_bwd_kernel(const BwdArgs a) {
     using Sm = BwdSmem<T>;
-    constexpr int RPW = 32 / LPR, S = Sm::S, V = Sm::V, NV = Sm::NV;
+    constexpr int RPW = 32 / LPR, S = Sm::S, E = 16 / sizeof(T);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
     asm volatile("griddepcontrol.launch_dependents;");  // the reduce waits for this grid's end
@@ -191,8 +197,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
         }
     }
     if (!dims_ok)  // lanes past the row's end add zeros to its sums
-        for (int i = 0; i < S; ++i)
-            for (int v = 0; v < NV; ++v) sm.ring[warp][i][v][lane] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2 * S; ++i)
+            for (int e = 0; e < 16; ++e) sm.ring[warp][i / 2][i % 2][rr * LPR * 16 + 16 * l + e] = T(0.f);
     const int hpw = 1 << sp.log_hpw;
     const int64_t step_x = hpw * a.x[side].sh, step_g = hpw * a.g[side].sh;
     const int64_t step_d = hpw * a.dx[side].sh;
@@ -213,9 +219,10 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
         at.c1 = min(sp.chunks, at.c + sp.per_part);
         at.tok = (int)min(grp * tpw + tsub, (int64_t)a.tokens);
     };
-    // The copying side runs S - 1 chunks ahead.
-    const uint32_t ring = smem_addr(&sm.ring[warp][0][0][lane]);
-    const T *px0 = nullptr, *px1 = nullptr, *pg0 = nullptr, *pg1 = nullptr;
+    // The copying side runs S - 1 chunks ahead; px and pg: this lane's first piece of its row.
+    const uint32_t ring = smem_addr(&sm.ring[warp][0][0][rr * LPR * 16 + E * l]);
+    const int pieces = a.D / E;
+    const T *px = nullptr, *pg = nullptr;
     At in{(int64_t)cta * kWarps + warp, 0, 0, 0};
     auto rows_in = [&]() {
         if (in.unit >= units) return;
@@ -223,29 +230,22 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
         const int t = in.tok < a.tokens ? in.tok : 0;
         const int b = a.tokens == a.T ? 0 : t / a.T;
         const int h = (in.c << sp.log_hpw) + hsub;
-        const T* x = a.x[side].row<T>(b, t - b * a.T) + h * a.x[side].sh;
-        const T* g = a.g[side].row<T>(b, t - b * a.T) + h * a.g[side].sh;
-        px0 = x + rl.off0;
-        px1 = x + rl.off1;
-        pg0 = g + rl.off0;
-        pg1 = g + rl.off1;
+        px = a.x[side].row<T>(b, t - b * a.T) + h * a.x[side].sh + E * l;
+        pg = a.g[side].row<T>(b, t - b * a.T) + h * a.g[side].sh + E * l;
     };
-    auto fetch = [&](int stage) {  // the next chunk, if there is one
+    auto fetch = [&](int stage) {  // the next chunk of rows, if there is one
         if (in.unit < units) {
-            if (in.tok < a.tokens && dims_ok && (in.c << sp.log_hpw) + hsub < sp.heads) {
-                const uint32_t dst = ring + (uint32_t)stage * (NV * 512);
+            if (in.tok < a.tokens && (in.c << sp.log_hpw) + hsub < sp.heads) {
+                const uint32_t dst = ring + (uint32_t)stage * (1024 * sizeof(T));
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    copy16(dst + i * 512, px0 + 4 * i);
-                    copy16(dst + (V + i) * 512, px1 + 4 * i);
-                    copy16(dst + (2 * V + i) * 512, pg0 + 4 * i);
-                    copy16(dst + (3 * V + i) * 512, pg1 + 4 * i);
-                }
+                for (int i = 0; i < (int)sizeof(T); ++i)
+                    if (l + i * LPR < pieces) {
+                        copy16(dst + i * LPR * 16, px + i * LPR * E);
+                        copy16(dst + 512 * sizeof(T) + i * LPR * 16, pg + i * LPR * E);
+                    }
             }
-            px0 += step_x;
-            px1 += step_x;
-            pg0 += step_g;
-            pg1 += step_g;
+            px += step_x;
+            pg += step_g;
             if (++in.c == in.c1) {
                 in.unit += stride;
                 rows_in();
@@ -294,13 +294,14 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
         added += at.c1 - at.c;
         for (int c = at.c; c < at.c1; ++c) {
             copy_wait<S - 2>();
-            const uint4* slot = &sm.ring[warp][stage][0][lane];
+            __syncwarp();  // the other lanes' pieces, and their reads of the stage before
+            const T* row = &sm.ring[warp][stage][0][rr * LPR * 16];
             f2 x0[4], x1[4], h0[4], h1[4];
-            pairs8<T>(slot, x0);
-            pairs8<T>(slot + 32 * V, x1);
-            pairs8<T>(slot + 64 * V, h0);
-            pairs8<T>(slot + 96 * V, h1);
-            // the slot read one chunk ago is free: every lane reads its own
+            pairs8(row + rl.off0, x0);
+            pairs8(row + rl.off1, x1);
+            pairs8(row + 512 + rl.off0, h0);
+            pairs8(row + 512 + rl.off1, h1);
+            // the stage read one chunk ago is free
             fetch(stage == 0 ? S - 1 : stage - 1);
             stage = stage + 1 == S ? 0 : stage + 1;
 
@@ -346,21 +347,19 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             // dx = (h r) w - x r k,  k = r^2 mean(g x);  dw += (h r) x
             const f2 r2 = f2_splat(r), nk = f2_splat(-(r * (r * (r * (dot * inv_d)))));
             if (ok && h < sp.heads) {
-                f2 d[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f2 hr = mul2(h0[i], r2);
                     acc[i] = fma2(hr, x0[i], acc[i]);
-                    d[i] = fma2(x0[i], nk, mul2(hr, w0[i]));
+                    x0[i] = fma2(x0[i], nk, mul2(hr, w0[i]));
                 }
-                store8<T>(d0, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f2 hr = mul2(h1[i], r2);
                     acc[4 + i] = fma2(hr, x1[i], acc[4 + i]);
-                    d[i] = fma2(x1[i], nk, mul2(hr, w1[i]));
+                    x1[i] = fma2(x1[i], nk, mul2(hr, w1[i]));
                 }
-                store8<T>(d1, d);
+                store_row<T, NB>(d0, d1, x0, x1, a.wide);
             }
             h += hpw;
             d0 += step_d;
@@ -447,6 +446,16 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
     if (lane == 0 && out < D) (blockIdx.y ? dwk : dwq)[out] = __fadd_rn(h, e);
 }
 
+// Whether every row of both outputs starts on 32 bytes.
+bool rows_on_32_bytes(const Heads (&y)[2], int dt) {
+    const uintptr_t e = dt == 1 ? 2 : 4;
+    for (const Heads& h : y)
+        if ((reinterpret_cast<uintptr_t>(h.p) | (uintptr_t)h.sb * e | (uintptr_t)h.st * e |
+             (uintptr_t)h.sh * e) % 32 != 0)
+            return false;
+    return true;
+}
+
 template <typename T, int LPR, bool NB>
 cudaError_t run_fwd(const QkCall& c, cudaStream_t s) {
     constexpr int RPW = 32 / LPR;
@@ -468,6 +477,7 @@ cudaError_t run_fwd(const QkCall& c, cudaStream_t s) {
     a.T = (int)c.T;
     a.D = c.D;
     a.w_bf16 = c.w_dt;
+    a.wide = rows_on_32_bytes(c.y, c.x_dt);
     a.eps = c.eps;
     qk_fwd_kernel<T, LPR, NB>
         <<<dim3((unsigned)gx, a.span[0].parts + a.span[1].parts), kWarps * 32, 0, s>>>(a);
@@ -516,6 +526,7 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
     a.T = (int)c.T;
     a.D = c.D;
     a.w_bf16 = c.w_dt;
+    a.wide = rows_on_32_bytes(c.y, c.x_dt);
     a.eps = c.eps;
     kernel<<<a.grid[0] + a.grid[1], kWarps * 32, sizeof(BwdSmem<T>), s>>>(a);
     e = cudaGetLastError();

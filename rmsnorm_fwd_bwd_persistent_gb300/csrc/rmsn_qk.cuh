@@ -155,7 +155,8 @@ struct Heads {
     int64_t sb, st, sh;
     template <typename T>
     __device__ __forceinline__ T* row(int b, int t) const {
-        return static_cast<T*>(p) + b * sb + t * st;
+        T* r = static_cast<T*>(p) + t * st;
+        return b ? r + b * sb : r;
     }
 };
 
@@ -244,26 +245,49 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Eight elements at a lane's place in its ring, as FP32 pairs, and back to memory.
-template <typename T>
-__device__ __forceinline__ void pairs8(const uint4* p, f2 (&f)[4]) {
-    if constexpr (sizeof(T) == 2) {
-        Pairs<__nv_bfloat16>::get(p[0], f);
+// Eight elements in shared memory as FP32 pairs.
+__device__ __forceinline__ void pairs8(const __nv_bfloat16* p, f2 (&f)[4]) {
+    Pairs<__nv_bfloat16>::get(*reinterpret_cast<const uint4*>(p), f);
+}
+__device__ __forceinline__ void pairs8(const float* p, f2 (&f)[4]) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2*>(p)[0];
+    const ulonglong2 b = reinterpret_cast<const ulonglong2*>(p)[1];
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
+}
+
+// 32 bytes to memory: at once, or in halves where they start on 16 bytes only.
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x),
+                     "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
     } else {
-        const uint4 a = p[0], b = p[32];
-        f[0] = f2_make(__uint_as_float(a.x), __uint_as_float(a.y));
-        f[1] = f2_make(__uint_as_float(a.z), __uint_as_float(a.w));
-        f[2] = f2_make(__uint_as_float(b.x), __uint_as_float(b.y));
-        f[3] = f2_make(__uint_as_float(b.z), __uint_as_float(b.w));
+        reinterpret_cast<uint4*>(p)[0] = a;
+        reinterpret_cast<uint4*>(p)[1] = b;
     }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const f2 (&f)[4]) {
+
+// A lane's two vectors to memory.  Vectors that lie together (neighbouring pairs) and FP32
+// vectors are 32 bytes of one lane, stored at once so that whole sectors are written.
+template <typename T, bool NEIGHBOURS>
+__device__ __forceinline__ void store_row(T* p0, T* p1, const f2 (&u)[4], const f2 (&v)[4], bool wide) {
     if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4*>(p) = Pairs<__nv_bfloat16>::put(f);
+        const uint4 a = Pairs<__nv_bfloat16>::put(u), b = Pairs<__nv_bfloat16>::put(v);
+        if (NEIGHBOURS) {
+            store32(p0, a, b, wide);
+        } else {
+            *reinterpret_cast<uint4*>(p0) = a;
+            *reinterpret_cast<uint4*>(p1) = b;
+        }
     } else {
-        reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(f[0], f[1]);
-        reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(f[2], f[3]);
+        auto half = [](f2 x, f2 y) {
+            return make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+        };
+        store32(p0, half(u[0], u[1]), half(u[2], u[3]), wide);
+        store32(p1, half(v[0], v[1]), half(v[2], v[3]), wide);
     }
 }
 
