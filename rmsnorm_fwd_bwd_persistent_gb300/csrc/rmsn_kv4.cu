@@ -330,41 +330,38 @@ struct UnitAt {
     }
 };
 
-// A tensor's rows streamed through a ring in shared memory that belongs to the lane alone: S
-// stages of one chunk, copied asynchronously S - 1 chunks ahead (across units too), so the bytes
-// in flight cost neither registers nor barriers.  Rows that do not exist are not copied; what
-// their places hold is not used.
-template <int S>
+// A tensor's rows streamed through a ring in shared memory that belongs to the warp: S stages of
+// one chunk, copied asynchronously S - 1 chunks ahead (across units too), so the bytes in flight
+// cost neither registers nor CTA barriers.  The lanes of a row copy it piece by piece in the order
+// of memory.  Rows that do not exist are not copied; what their places hold is not used.
+template <int S, int LPR>
 struct RowStream {
-    using Ring = uint4[S][2][32];  // of one warp
+    using Ring = bf16[S][512];  // of one warp: its rows one after the other
 
-    const bf16 *p0, *p1;
+    const bf16* p;  // this lane's first piece of its row
     int64_t step, stride, units;
     UnitAt in;
     uint32_t ring;
     int hsub, tsub, tpw;
 
-    __device__ __forceinline__ void rows(const Heads& x, const Span& sp, int off0, int off1, int tokens) {
+    __device__ __forceinline__ void rows(const Heads& x, const Span& sp, int tokens) {
         if (in.unit >= units) return;
         in.enter(sp, tpw, tsub, tokens);
-        const bf16* row = x.row<bf16>(0, in.tok < tokens ? in.tok : 0) + ((in.c << sp.log_hpw) + hsub) * x.sh;
-        p0 = row + off0;
-        p1 = row + off1;
+        p = x.row<bf16>(0, in.tok < tokens ? in.tok : 0) + ((in.c << sp.log_hpw) + hsub) * x.sh +
+            8 * (threadIdx.x % LPR);
     }
 
     // Copies the next chunk, if there is one, to a stage.
-    __device__ __forceinline__ void fetch(int stage, const Heads& x, const Span& sp, int off0, int off1,
-                                          int tokens) {
+    __device__ __forceinline__ void fetch(int stage, const Heads& x, const Span& sp, int tokens) {
         if (in.unit < units) {
             if (in.tok < tokens && (in.c << sp.log_hpw) + hsub < sp.heads) {
-                copy16(ring + (uint32_t)stage * 1024, p0);
-                copy16(ring + (uint32_t)stage * 1024 + 512, p1);
+                copy16(ring + (uint32_t)stage * 1024, p);
+                copy16(ring + (uint32_t)stage * 1024 + 16 * LPR, p + 8 * LPR);
             }
-            p0 += step;
-            p1 += step;
+            p += step;
             if (++in.c == in.c1) {
                 in.unit += stride;
-                rows(x, sp, off0, off1, tokens);
+                rows(x, sp, tokens);
             }
         }
         copy_commit();
@@ -375,7 +372,7 @@ constexpr int kAppendStages = 6;  // 6 KiB per warp
 constexpr int kStreamFrom = 4;    // units per warp from which the streaming kernel is taken
 
 struct AppendSmem {
-    RowStream<kAppendStages>::Ring ring[kWarps];
+    bf16 ring[kWarps][kAppendStages][512];
     bf16 turn[kWarps][512];  // rows of k on their way to neighbouring dims
 };
 
@@ -400,8 +397,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const Ap
     RowLane<NB> rl;
     rl.init(l, side == 2 ? 0 : a.rope.rd);
     const Heads& x = a.x[side];
-    RowStream<S> rows;
-    rows.ring = smem_addr(&sm.ring[warp][0][0][lane]);
+    RowStream<S, LPR> rows;
+    rows.ring = smem_addr(&sm.ring[warp][0][rr * D + 8 * l]);
     rows.stride = stride;
     rows.units = units;
     rows.hsub = hsub;
@@ -409,9 +406,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const Ap
     rows.tpw = tpw;
     rows.step = (int64_t)(1 << sp.log_hpw) * x.sh;
     rows.in.unit = first;
-    rows.rows(x, sp, rl.off0, rl.off1, a.tokens);
+    rows.rows(x, sp, a.tokens);
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) rows.fetch(i, x, sp, rl.off0, rl.off1, a.tokens);
+    for (int i = 0; i < S - 1; ++i) rows.fetch(i, x, sp, a.tokens);
     f2 w0[4], w1[4];
     load_weights(a.w[side & 1], a.w_bf16, rl.off0, rl.off1, side < 2, w0, w1);
     const int hpw = 1 << sp.log_hpw;
@@ -446,10 +443,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const Ap
         rec += h * head_bytes;
         for (int c = at.c; c < at.c1; ++c) {
             copy_wait<S - 2>();
-            const uint4* slot = &sm.ring[warp][stage][0][lane];
-            Raw8<bf16> r0{slot[0]}, r1{slot[32]};
-            // the stage read one chunk ago is free: every lane reads its own
-            rows.fetch(stage == 0 ? S - 1 : stage - 1, x, sp, rl.off0, rl.off1, a.tokens);
+            __syncwarp();  // the other lanes' pieces, and their reads of the stage before
+            const bf16* row = &sm.ring[warp][stage][rr * D];
+            Raw8<bf16> r0{*reinterpret_cast<const uint4*>(row + rl.off0)};
+            Raw8<bf16> r1{*reinterpret_cast<const uint4*>(row + rl.off1)};
+            // the stage read one chunk ago is free
+            rows.fetch(stage == 0 ? S - 1 : stage - 1, x, sp, a.tokens);
             stage = stage + 1 == S ? 0 : stage + 1;
             const bool row_ok = ok && h < sp.heads;
             if (side < 2) {
