@@ -18,10 +18,10 @@ import torch
 from . import attn as _attn
 from .attn import (  # noqa: F401  (public entry points)
     KV4_BLOCK, KV4_GROUP, kv4_attention, kv4_attention_workspace_bytes, kv4_cache_shape, kv4_read,
-    qk_norm_rope_bwd, qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_fwd, qk_norm_rope_kv4_append)
+    load_binding,    qk_norm_rope_bwd, qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_fwd, qk_norm_rope_kv4_append)
 
 __all__ = [
-    "RMSN_F32", "RMSN_BF16", "RMSN_MAX_H", "RmsnError", "library_path", "load_library",
+    "RMSN_F32", "RMSN_BF16", "RMSN_MAX_H", "RmsnError", "library_path", "load_library", "load_binding",
     "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_bwd_workspace_bytes",
     "rmsnorm_fwd_residual", "rmsnorm_bwd_residual",
     "fused_add_rmsnorm_fp8_block_quant", "rmsn_status_string", "rmsn_plan", "rmsn_set_policy",

@@ -60,7 +60,7 @@ def declare(L) -> None:
 _module = None
 
 
-def _native():
+def load_binding():
     """The compiled module (``csrc/rmsn_binding.cpp``); raises if it was not built."""
     global _module
     if _module is None:
@@ -109,7 +109,7 @@ def qk_norm_rope_fwd(q, k, wq, wk, cos, sin, positions, eps: float = 1e-6, *,
                 or (2i, 2i + 1) with interleaved=True
     positions   int64 [T] or [B, S]: the table row of every token
     q_out and k_out may be q and k themselves.  Returns (q_out, k_out)."""
-    return _done(_native().qk_norm_rope_fwd(q, k, wq, wk, cos, sin, positions, eps, interleaved,
+    return _done(load_binding().qk_norm_rope_fwd(q, k, wq, wk, cos, sin, positions, eps, interleaved,
                                             q_out, k_out), "qk_norm_rope_fwd")
 
 
@@ -122,7 +122,7 @@ def qk_norm_rope_bwd(gq, gk, q, k, wq, wk, cos, sin, positions, eps: float = 1e-
                      dwk=None):
     """Gradients of qk_norm_rope_fwd at (q, k) for the gradients gq and gk of its outputs.
     Returns (dq, dk, dwq, dwk); dwq and dwk are float32 [D] (overwritten)."""
-    return _done(_native().qk_norm_rope_bwd(gq, gk, q, k, wq, wk, cos, sin, positions, eps,
+    return _done(load_binding().qk_norm_rope_bwd(gq, gk, q, k, wq, wk, cos, sin, positions, eps,
                                             interleaved, workspace, dq, dk, dwq, dwk),
                  "qk_norm_rope_bwd")
 
@@ -142,7 +142,7 @@ def qk_norm_rope_kv4_append(q, k, v, wq, wk, cos, sin, positions, cache, slots,
     rotated k and the v as they are to `cache` in 4 bits at `slots` (int64 [T]: page * page_size +
     place in the page; negative: the token is padding and nothing is done for it, its q_out row
     included).  q, k, v are bfloat16 [T, heads, D] by any strides; q_out may be q."""
-    return _done(_native().qk_norm_rope_kv4_append(q, k, v, wq, wk, cos, sin, positions, cache, slots,
+    return _done(load_binding().qk_norm_rope_kv4_append(q, k, v, wq, wk, cos, sin, positions, cache, slots,
                                                    eps, interleaved, q_out),
                  "qk_norm_rope_kv4_append")[0]
 
@@ -150,7 +150,7 @@ def qk_norm_rope_kv4_append(q, k, v, wq, wk, cos, sin, positions, cache, slots,
 def kv4_read(cache, slots, k=None, v=None):
     """The K and V stored at `slots` (int64 [T]) as bfloat16 [T, kv heads, D]: (k, v).  Rows of a
     negative slot stay as they were."""
-    return _done(_native().kv4_read(cache, slots, k, v), "kv4_read")
+    return _done(load_binding().kv4_read(cache, slots, k, v), "kv4_read")
 
 
 def kv4_attention_workspace_bytes(seqs: int, D: int, device=None) -> int:
@@ -170,5 +170,5 @@ def kv4_attention(q, cache, page_table, kv_lens, *, cu_q=None, max_q: int = 1,
     scale       of the scores, 1/sqrt(D) where None
     Returns (out bfloat16 [T, heads, D], lse float32 [T, heads]); a query that sees no token gives
     0 and -inf, rows that no sequence has stay as they were."""
-    return _done(_native().kv4_attention(q, cache, page_table, kv_lens, cu_q, max_q, scale, out, lse,
+    return _done(load_binding().kv4_attention(q, cache, page_table, kv_lens, cu_q, max_q, scale, out, lse,
                                          workspace), "kv4_attention")

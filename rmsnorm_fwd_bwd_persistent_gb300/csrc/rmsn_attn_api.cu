@@ -17,6 +17,16 @@ constexpr int64_t kMaxStride = (int64_t)1 << 40;  // elements; keeps every produ
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool valid_dtype(int dt) { return dt == RMSN_F32 || dt == RMSN_BF16; }
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? RMSN_OK : RMSN_ERR_CUDA; }
+
+// Runs a launcher; nothing it may throw (its caches allocate) leaves a C entry point.
+template <typename F>
+int launched(F f) {
+    try {
+        return from_cuda(f());
+    } catch (...) {
+        return RMSN_ERR_CUDA;
+    }
+}
 bool head_size_ok(int64_t D) { return D >= 16 && D <= 256 && D % 16 == 0; }
 bool cache_head_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
 
@@ -36,6 +46,10 @@ int check_heads(const rmsn_heads_t* h, int64_t B, int64_t T, int64_t D, int dt, 
         if (a.s < 0 || a.s > kMaxStride) return RMSN_ERR_INVALID_ARG;
         if (a.s % vec != 0) return RMSN_ERR_MISALIGNED;
     }
+    // what the strides span stays far from 64 bits (an axis has below 2^31 steps of 2^40 at most)
+    __int128 extent = D;
+    for (const Axis& a : ax) extent += (__int128)(a.n > 1 ? a.n - 1 : 0) * a.s;
+    if (extent > ((__int128)1 << 47)) return RMSN_ERR_INVALID_ARG;
     out->p = h->data;
     out->sb = ax[0].s;
     out->st = ax[1].s;
@@ -148,7 +162,7 @@ int qk_norm_rope_fwd(const rmsn_heads_t* q, const rmsn_heads_t* k, int x_dtype, 
     if (c.tokens == 0) return RMSN_OK;
     uint64_t limit;
     RMSN_CHECK(rmsn::device_facts(&c.sms, &c.err, &limit));
-    return from_cuda(rmsn::launch_qk(c, reinterpret_cast<cudaStream_t>(stream)));
+    return launched([&] { return rmsn::launch_qk(c, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 size_t qk_norm_rope_bwd_workspace_bytes(int64_t D, int device) {
@@ -189,7 +203,7 @@ int qk_norm_rope_bwd(const rmsn_heads_t* gq, const rmsn_heads_t* gk, const rmsn_
     c.ws = static_cast<float*>(workspace);
     c.dw[0] = dwq;
     c.dw[1] = dwk;
-    return from_cuda(rmsn::launch_qk(c, s));
+    return launched([&] { return rmsn::launch_qk(c, s); });
 }
 
 int qk_norm_rope_kv4_append(const rmsn_heads_t* q, const rmsn_heads_t* k, const rmsn_heads_t* v,
@@ -227,7 +241,7 @@ int qk_norm_rope_kv4_append(const rmsn_heads_t* q, const rmsn_heads_t* k, const 
     c.w_dt = w_dtype;
     c.neighbours = rope->neighbours != 0;
     c.eps = eps;
-    return from_cuda(rmsn::launch_kv4_append(c, reinterpret_cast<cudaStream_t>(stream)));
+    return launched([&] { return rmsn::launch_kv4_append(c, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 int kv4_read(const rmsn_kv4_t* cache, const int64_t* slots, const rmsn_heads_t* k,
@@ -251,7 +265,7 @@ int kv4_read(const rmsn_kv4_t* cache, const int64_t* slots, const rmsn_heads_t* 
     c.kv_heads = (int)cache->kv_heads;
     c.blocks_per_page = (int)(cache->page_size / rmsn::kKv4Block);
     c.D = (int)D;
-    return from_cuda(rmsn::launch_kv4_read(c, reinterpret_cast<cudaStream_t>(stream)));
+    return launched([&] { return rmsn::launch_kv4_read(c, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 size_t kv4_attention_workspace_bytes(int64_t seqs, int64_t D, int device) {
@@ -317,7 +331,7 @@ int kv4_attention(const rmsn_heads_t* q, const rmsn_kv4_t* cache, const int32_t*
     c.max_q = (int)(max_q < T ? max_q : T);
     c.D = (int)D;
     c.scale = scale;
-    return from_cuda(rmsn::launch_kv4_attention(c, reinterpret_cast<cudaStream_t>(stream)));
+    return launched([&] { return rmsn::launch_kv4_attention(c, reinterpret_cast<cudaStream_t>(stream)); });
 }
 
 }  // extern "C"

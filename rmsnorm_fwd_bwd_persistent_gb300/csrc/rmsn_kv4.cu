@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
     const int r = (int)(slot & (kKv4Block - 1));
 
     Angles ang;
-    float w0[8], w1[8];
+    f2 w0[4], w1[4];
     bool have = false;
     for (int c = part * sp.per_part; c < c1; c += U) {
         Raw8<bf16> r0[U], r1[U];
@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
                 const int64_t at = tk.pos * (a.rope.rd / 2) + 8 * l;
                 ang.load(a.rope.cos + at, a.rope.sin + at);
             }
-            load_w8(a.w[side], a.w_bf16, rl.off0, w0);
-            load_w8(a.w[side], a.w_bf16, rl.off1, w1);
+            load_weights(a.w[side], a.w_bf16, rl.off0, rl.off1, true, w0, w1);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -199,23 +198,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
             const int h = ((c + i) << sp.log_hpw) + hsub;
             const bool row_ok = ok && h < sp.heads;
             if (side < 2) {
-                float u[8], v[8];
-                r0[i].get(u);
-                r1[i].get(v);
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-                const float rs = row_rstd(row_sum<LPR>(ss), 1.f / D, a.eps);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    u[e] = u[e] * rs * w0[e];
-                    v[e] = v[e] * rs * w1[e];
-                }
-                rotate<NB, false>(u, v, ang);
-                r0[i].set(u);
-                r1[i].set(v);
+                f2 u[4], v[4];
+                r0[i].pairs(u);
+                r1[i].pairs(v);
+                norm_rotate<NB, LPR>(u, v, w0, w1, ang, 1.f / D, a.eps);
+                r0[i].a = Pairs<bf16>::put(u);
+                r1[i].a = Pairs<bf16>::put(v);
                 if (side == 0) {
                     if (row_ok) {
                         r0[i].store(y + h * syh + rl.off0);
@@ -238,78 +226,6 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_append_kernel(const AppendArg
             if (!row_ok) continue;
             put16<D>(rec0 + h * head_bytes, r, l, side == 1, word, sm);
         }
-    }
-}
-
-// rotate() on pairs.  (Half pairs: the lane's vectors are the partners, two at a time;
-// neighbours: one at a time.)
-template <bool NEIGHBOURS, bool TRANSPOSE>
-__device__ __forceinline__ void rotate2(f2 (&u)[4], f2 (&v)[4], const Angles& t) {
-    if constexpr (NEIGHBOURS) {
-        float a[8], b[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[2 * i] = f2_lo(u[i]);
-            a[2 * i + 1] = f2_hi(u[i]);
-            b[2 * i] = f2_lo(v[i]);
-            b[2 * i + 1] = f2_hi(v[i]);
-        }
-        rotate<true, TRANSPOSE>(a, b, t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            u[i] = f2_make(a[2 * i], a[2 * i + 1]);
-            v[i] = f2_make(b[2 * i], b[2 * i + 1]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f2 c = f2_make(t.c[2 * i], t.c[2 * i + 1]);
-            const f2 s = f2_make(t.s[2 * i], t.s[2 * i + 1]);
-            const f2 x = u[i], y = v[i];
-            if (TRANSPOSE) {
-                u[i] = fma2(y, s, mul2(x, c));
-                v[i] = sub2(mul2(y, c), mul2(x, s));
-            } else {
-                u[i] = sub2(mul2(x, c), mul2(y, s));
-                v[i] = fma2(x, s, mul2(y, c));
-            }
-        }
-    }
-}
-
-// (x r) w, rotated: the forward of one row's lane.
-template <bool NEIGHBOURS, int LPR>
-__device__ __forceinline__ void norm_rotate(f2 (&u)[4], f2 (&v)[4], const f2 (&w0)[4], const f2 (&w1)[4],
-                                            const Angles& ang, float inv_d, float eps) {
-    f2 ss2 = 0ull;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ss2 = fma2(u[i], u[i], ss2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ss2 = fma2(v[i], v[i], ss2);
-    const float r = row_rstd(row_sum<LPR>(f2_lo(ss2) + f2_hi(ss2)), inv_d, eps);
-    const f2 r2 = f2_splat(r);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        u[i] = mul2(mul2(u[i], r2), w0[i]);
-        v[i] = mul2(mul2(v[i], r2), w1[i]);
-    }
-    rotate2<NEIGHBOURS, false>(u, v, ang);
-}
-
-// The weights beside a lane's two vectors (zero where it has none).
-__device__ __forceinline__ void load_weights(const void* w, int bf16, int off0, int off1, bool ok,
-                                             f2 (&w0)[4], f2 (&w1)[4]) {
-    float f0[8], f1[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f0[i] = f1[i] = 0.f;
-    if (ok) {
-        load_w8(w, bf16, off0, f0);
-        load_w8(w, bf16, off1, f1);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w0[i] = f2_make(f0[2 * i], f0[2 * i + 1]);
-        w1[i] = f2_make(f1[2 * i], f1[2 * i + 1]);
     }
 }
 

@@ -828,8 +828,9 @@ __global__ void __launch_bounds__(combine_threads(WIDE)) kv4_combine_kernel(cons
     const int64_t per = share_of(a.prefix[a.seqs], ctas);
     const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * (s.units + kItemCost) + kItemCost;
     const int64_t u1 = u0 + s.units - 1;
-    const int c0 = u1 >> 32 ? (int)(u0 / per) : (int)((uint32_t)u0 / (uint32_t)per);
-    const int c1 = u1 >> 32 ? (int)(u1 / per) : (int)((uint32_t)u1 / (uint32_t)per);
+    const bool big = ((u1 | per) >> 32) != 0;
+    const int c0 = big ? (int)(u0 / per) : (int)((uint32_t)u0 / (uint32_t)per);
+    const int c1 = big ? (int)(u1 / per) : (int)((uint32_t)u1 / (uint32_t)per);
     if (c0 == c1) return;
     float m = -FLT_MAX, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -38,7 +38,7 @@ struct FwdArgs {
 // One unit of work per warp: tpw tokens and the chunks [part * per_part, ...) of their heads.
 // blockIdx.y picks q or k and the part, blockIdx.x and the warp the tokens.
 template <typename T, int LPR, bool NB>
-__global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 5) qk_fwd_kernel(const FwdArgs a) {
     constexpr int RPW = 32 / LPR;
     constexpr int U = sizeof(T) == 2 ? 4 : 2;  // chunks in flight: 4 KiB of rows per warp
     const int side = blockIdx.y < a.span[0].parts ? 0 : 1;
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
 
     const float inv_d = __frcp_rn((float)a.D);
     Angles ang;
-    float w0[8], w1[8];
+    f2 w0[4], w1[4];
     bool have = false;
     for (int c = part * sp.per_part; c < c1; c += U) {
         Raw8<T> r0[U], r1[U];
@@ -79,46 +79,23 @@ __global__ void __launch_bounds__(kWarps * 32) qk_fwd_kernel(const FwdArgs a) {
         if (!have) {  // after the first rows are on their way
             have = true;
             ang.identity();
-            if (lane_ok) {
-                if (rl.turns) {
-                    const int64_t at = tk.pos * (a.rope.rd / 2) + 8 * l;
-                    ang.load(a.rope.cos + at, a.rope.sin + at);
-                }
-                load_w8(a.w[side], a.w_bf16, rl.off0, w0);
-                load_w8(a.w[side], a.w_bf16, rl.off1, w1);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w0[i] = w1[i] = 0.f;
+            if (lane_ok && rl.turns) {
+                const int64_t at = tk.pos * (a.rope.rd / 2) + 8 * l;
+                ang.load(a.rope.cos + at, a.rope.sin + at);
             }
+            load_weights(a.w[side], a.w_bf16, rl.off0, rl.off1, lane_ok, w0, w1);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int h = ((c + i) << sp.log_hpw) + hsub;
             if (c + i >= c1) break;  // the same for the whole warp
-            float u[8], v[8];
-            r0[i].get(u);
-            r1[i].get(v);
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
-            const float r = row_rstd(row_sum<LPR>(ss), inv_d, a.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                u[e] = u[e] * r * w0[e];
-                v[e] = v[e] * r * w1[e];
-            }
-            rotate<NB, false>(u, v, ang);
+            f2 u[4], v[4];
+            r0[i].pairs(u);
+            r1[i].pairs(v);
+            norm_rotate<NB, LPR>(u, v, w0, w1, ang, inv_d, a.eps);
             if (lane_ok && h < sp.heads) {
-                f2 y0[4], y1[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y0[e] = f2_make(u[2 * e], u[2 * e + 1]);
-                    y1[e] = f2_make(v[2 * e], v[2 * e + 1]);
-                }
                 T* to = y + h * syh;
-                store_row<T, NB>(to + rl.off0, to + rl.off1, y0, y1, a.wide);
+                store_row<T, NB>(to + rl.off0, to + rl.off1, u, v, a.wide);
             }
         }
     }
@@ -181,21 +158,10 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
     RowLane<NB> rl;
     rl.init(l, a.rope.rd);
     f2 w0[4], w1[4], acc[8];
-    {
-        float f0[8], f1[8];
+    load_weights(a.w[side], a.w_bf16, rl.off0, rl.off1, dims_ok, w0, w1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f0[i] = f1[i] = 0.f;
-        if (dims_ok) {
-            load_w8(a.w[side], a.w_bf16, rl.off0, f0);
-            load_w8(a.w[side], a.w_bf16, rl.off1, f1);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w0[i] = f2_make(f0[2 * i], f0[2 * i + 1]);
-            w1[i] = f2_make(f1[2 * i], f1[2 * i + 1]);
-            sm.sums[0][i][threadIdx.x] = sm.sums[1][i][threadIdx.x] = make_ulonglong2(0ull, 0ull);
-        }
-    }
+    for (int i = 0; i < 4; ++i)
+        sm.sums[0][i][threadIdx.x] = sm.sums[1][i][threadIdx.x] = make_ulonglong2(0ull, 0ull);
     if (!dims_ok)  // lanes past the row's end add zeros to its sums
         for (int i = 0; i < 2 * S; ++i)
             for (int e = 0; e < 16; ++e) sm.ring[warp][i / 2][i % 2][rr * LPR * 16 + 16 * l + e] = T(0.f);
@@ -305,31 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             fetch(stage == 0 ? S - 1 : stage - 1);
             stage = stage + 1 == S ? 0 : stage + 1;
 
-            if constexpr (NB) {
-                float u[8], v[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u[2 * i] = f2_lo(h0[i]);
-                    u[2 * i + 1] = f2_hi(h0[i]);
-                    v[2 * i] = f2_lo(h1[i]);
-                    v[2 * i + 1] = f2_hi(h1[i]);
-                }
-                rotate<true, true>(u, v, ang);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h0[i] = f2_make(u[2 * i], u[2 * i + 1]);
-                    h1[i] = f2_make(v[2 * i], v[2 * i + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f2 cc = f2_make(ang.c[2 * i], ang.c[2 * i + 1]);
-                    const f2 s2 = f2_make(ang.s[2 * i], ang.s[2 * i + 1]);
-                    const f2 y = h0[i];
-                    h0[i] = fma2(h1[i], s2, mul2(y, cc));
-                    h1[i] = sub2(mul2(h1[i], cc), mul2(y, s2));
-                }
-            }
+            rotate2<NB, true>(h0, h1, ang);
             f2 ss2 = 0ull, dot2 = 0ull;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

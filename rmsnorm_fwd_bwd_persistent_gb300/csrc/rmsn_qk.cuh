@@ -31,7 +31,7 @@ struct Raw8<__nv_bfloat16> {
     }
     __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void get(float (&f)[8]) const { Elem<__nv_bfloat16>::unpack(a, f); }
-    __device__ __forceinline__ void set(const float (&f)[8]) { a = Elem<__nv_bfloat16>::pack(f); }
+    __device__ __forceinline__ void pairs(f2 (&f)[4]) const { Pairs<__nv_bfloat16>::get(a, f); }
     __device__ __forceinline__ void store(__nv_bfloat16* p) const {
         *reinterpret_cast<uint4*>(p) = a;
     }
@@ -48,13 +48,11 @@ struct Raw8<float> {
         f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
         f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
     }
-    __device__ __forceinline__ void set(const float (&f)[8]) {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ void store(float* p) const {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
+    __device__ __forceinline__ void pairs(f2 (&f)[4]) const {
+        f[0] = f2_make(a.x, a.y);
+        f[1] = f2_make(a.z, a.w);
+        f[2] = f2_make(b.x, b.y);
+        f[3] = f2_make(b.z, b.w);
     }
 };
 
@@ -100,8 +98,14 @@ template <bool NEIGHBOURS, bool TRANSPOSE>
 __device__ __forceinline__ void rotate(float (&u)[8], float (&v)[8], const Angles& t) {
     auto turn = [](float& a, float& b, float c, float s) {
         const float x = a, y = b;
-        a = TRANSPOSE ? fmaf(y, s, x * c) : fmaf(-y, s, x * c);
-        b = TRANSPOSE ? fmaf(-x, s, y * c) : fmaf(x, s, y * c);
+        // (as rotate2 rounds: one component by two products and a difference)
+        if (TRANSPOSE) {
+            a = fmaf(y, s, __fmul_rn(x, c));
+            b = __fsub_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+        } else {
+            a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+            b = fmaf(x, s, __fmul_rn(y, c));
+        }
     };
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -288,6 +292,79 @@ __device__ __forceinline__ void store_row(T* p0, T* p1, const f2 (&u)[4], const 
         };
         store32(p0, half(u[0], u[1]), half(u[2], u[3]), wide);
         store32(p1, half(v[0], v[1]), half(v[2], v[3]), wide);
+    }
+}
+
+// rotate() on pairs.  (Half pairs: the lane's vectors are the partners, two at a time;
+// neighbours: one at a time.)
+template <bool NEIGHBOURS, bool TRANSPOSE>
+__device__ __forceinline__ void rotate2(f2 (&u)[4], f2 (&v)[4], const Angles& t) {
+    if constexpr (NEIGHBOURS) {
+        float a[8], b[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[2 * i] = f2_lo(u[i]);
+            a[2 * i + 1] = f2_hi(u[i]);
+            b[2 * i] = f2_lo(v[i]);
+            b[2 * i + 1] = f2_hi(v[i]);
+        }
+        rotate<true, TRANSPOSE>(a, b, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = f2_make(a[2 * i], a[2 * i + 1]);
+            v[i] = f2_make(b[2 * i], b[2 * i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f2 c = f2_make(t.c[2 * i], t.c[2 * i + 1]);
+            const f2 s = f2_make(t.s[2 * i], t.s[2 * i + 1]);
+            const f2 x = u[i], y = v[i];
+            if (TRANSPOSE) {
+                u[i] = fma2(y, s, mul2(x, c));
+                v[i] = sub2(mul2(y, c), mul2(x, s));
+            } else {
+                u[i] = sub2(mul2(x, c), mul2(y, s));
+                v[i] = fma2(x, s, mul2(y, c));
+            }
+        }
+    }
+}
+
+// (x r) w, rotated: the forward of one row's lane.  All forward kernels share it, so that a row
+// gets the same bits whichever of them it goes through.
+template <bool NEIGHBOURS, int LPR>
+__device__ __forceinline__ void norm_rotate(f2 (&u)[4], f2 (&v)[4], const f2 (&w0)[4], const f2 (&w1)[4],
+                                            const Angles& ang, float inv_d, float eps) {
+    f2 ss2 = 0ull;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss2 = fma2(u[i], u[i], ss2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ss2 = fma2(v[i], v[i], ss2);
+    const float r = row_rstd(row_sum<LPR>(f2_lo(ss2) + f2_hi(ss2)), inv_d, eps);
+    const f2 r2 = f2_splat(r);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u[i] = mul2(mul2(u[i], r2), w0[i]);
+        v[i] = mul2(mul2(v[i], r2), w1[i]);
+    }
+    rotate2<NEIGHBOURS, false>(u, v, ang);
+}
+
+// The weights beside a lane's two vectors (zero where it has none).
+__device__ __forceinline__ void load_weights(const void* w, int bf16, int off0, int off1, bool ok,
+                                             f2 (&w0)[4], f2 (&w1)[4]) {
+    float f0[8], f1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f0[i] = f1[i] = 0.f;
+    if (ok) {
+        load_w8(w, bf16, off0, f0);
+        load_w8(w, bf16, off1, f1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w0[i] = f2_make(f0[2 * i], f0[2 * i + 1]);
+        w1[i] = f2_make(f1[2 * i], f1[2 * i + 1]);
     }
 }
 

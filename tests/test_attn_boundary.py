@@ -72,6 +72,14 @@ def test_fwd_refusals(lib):
     assert fwd(lib, yq=heads(sb=256), B=2, T=2) == INVALID
 
 
+def test_strides_that_would_leave_64_bits_are_refused(lib):
+    far = (1 << 40) - 8
+    assert fwd(lib, q=heads(st=far), yq=heads(), T=1 << 30) == INVALID
+    assert fwd(lib, yq=heads(st=far), T=1 << 30) == INVALID
+    assert fwd(lib, q=heads(sb=far), yq=heads(sb=512), yk=heads(2, sb=256), B=1 << 20, T=2) == INVALID
+    assert fwd(lib, q=heads(st=(1 << 40) + 8), yq=heads(), T=2) == INVALID
+
+
 def test_rope_refusals(lib):
     for rd in (0, 8, 24, 80, -16):
         assert fwd(lib, r=rope(rd=rd)) == SHAPE

@@ -250,6 +250,57 @@ def test_long_and_ragged(Hq, Hk, D, ps):
     check(torch.randn(len(lens), Hq, D, generator=g).to(BF16), cache, table, lens)
 
 
+def test_a_chunk_of_a_prompt():
+    """Far more query tokens than max_q says, in many blocks of columns, beside single ones."""
+    lens, cu = [333, 40, 200], [0, 200, 201, 250]
+    for Hq, Hk, D in ((8, 2, 128), (6, 2, 64), (2, 1, 256)):
+        cache, table, g = filled(lens, Hk, 16, D, seed=D)
+        check(torch.randn(250, Hq, D, generator=g).to(BF16), cache, table, lens, cu, max_q=1)
+
+
+def test_calls_on_two_streams():
+    """Two calls at once, each with its own buffers: the bits of the calls alone."""
+    lens = [4000, 300, 77]
+    cache, table, g = filled(lens, 4, 32, 128, seed=21)
+    c, t, n = cache.to(DEV), table.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = [torch.randn(3, 16, 128, generator=g).to(BF16).to(DEV) for _ in range(2)]
+    alone = [rmsn.kv4_attention(x, c, t, n) for x in q]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(side[i]):
+                outs[i].append(rmsn.kv4_attention(q[i], c, t, n))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o in outs[i]:
+            assert torch.equal(o[0], alone[i][0]) and torch.equal(o[1], alone[i][1])
+    assert rmsn.rmsn_device_status() == 0
+
+
+def test_graphs_that_share_a_workspace():
+    """Two graphs captured over one workspace and replayed in turn: what one leaves does not reach the other."""
+    long, short = filled([3000], 2, 16, 64, seed=22), filled([50, 0, 700], 2, 16, 64, seed=23)
+    runs = []
+    ws = torch.empty(rmsn.kv4_attention_workspace_bytes(3, 64), dtype=torch.uint8, device=DEV)
+    for (cache, table, g), lens in ((long, [3000]), (short, [50, 0, 700])):
+        a = (torch.randn(len(lens), 8, 64, generator=g).to(BF16).to(DEV), cache.to(DEV), table.to(DEV),
+             torch.tensor(lens, dtype=torch.int32, device=DEV))
+        eager = rmsn.kv4_attention(*a)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = rmsn.kv4_attention(*a, workspace=ws)
+        runs.append((graph, out, eager, a))
+    for _ in range(3):
+        for graph, out, eager, _ in runs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, eager, _ in runs:
+            assert torch.equal(out[0], eager[0]) and torch.equal(out[1], eager[1])
+
+
 def test_many_sequences():
     """More sequences than the threads of a CTA (two tiles of the work split's prefix sums)."""
     lens = [(i * 37) % 40 for i in range(300)]
@@ -456,6 +507,31 @@ def test_serving_path_in_a_graph():
         assert ((lse[:B].cpu().double() - rl).abs() <= lb + 2.0 ** -22 * rl.abs()).all()
         assert (out[B] == 0).all() and torch.isinf(lse[B]).all()
     assert rmsn.rmsn_device_status() == 0
+
+
+@pytest.mark.parametrize("T,nb", [(5000, False), (9000, True)])
+def test_long_append_streams(T, nb):
+    """Enough tokens for the streaming kernel, padding and a bad slot among them: the bytes of the small one."""
+    Hq, Hk, D, ps = 6, 2, 128, 16
+    x, (wq, wk), (cos, sin), pos, g = append_inputs(T, Hq, Hk, D, D, seed=T)
+    pages = -(-T // ps) + 1
+    slots = torch.randperm(pages * ps, generator=g)[:T]
+    slots[::97] = -1
+    slots[1234] = pages * ps
+    q, k, v = x.to(DEV).split([Hq, Hk, Hk], 1)
+    rest = [t.to(DEV) for t in (wq, wk, cos, sin)]
+    big, small = empty_cache(pages, Hk, ps, D), empty_cache(pages, Hk, ps, D)
+    yq = torch.full((T, Hq, D), 7.0, dtype=BF16, device=DEV)
+    rmsn.qk_norm_rope_kv4_append(q, k, v, *rest, pos.to(DEV), big, slots.to(DEV), EPS, interleaved=nb, q_out=yq)
+    assert rmsn.rmsn_device_status() == ERR_INDEX
+    zq = torch.full((T, Hq, D), 7.0, dtype=BF16, device=DEV)
+    for a in range(0, T, 100):
+        b = slice(a, a + 100)
+        rmsn.qk_norm_rope_kv4_append(q[b], k[b], v[b], *rest, pos[b].to(DEV), small, slots[b].to(DEV), EPS,
+                                     interleaved=nb, q_out=zq[b])
+    assert rmsn.rmsn_device_status() == ERR_INDEX
+    assert torch.equal(big, small) and torch.equal(yq, zq)
+    assert (yq[0] == 7).all() and (yq[1234] == 7).all()
 
 
 def test_cache_beyond_4_gib():
