@@ -155,6 +155,24 @@ def test_zero_and_extreme_rows():
     assert (yq[0] == 0).all()
 
 
+def test_rounding_of_the_reciprocal_root():
+    """One nonzero element per head, no rotation (cos = 1, sin = 0), w = 1: y = x (1 / sqrt(x^2 / 16 + eps)) with
+    every operation rounded once, so torch's IEEE square root and division on the CPU give the same bits."""
+    T, D = 20000, 16
+    g = gen(11)
+    v = torch.randn(T, 1, generator=g) * 10.0 ** torch.empty(T, 1).uniform_(-6, 6, generator=g)
+    x = torch.zeros(T, 1, D)
+    x[..., 3] = v
+    one, zero = torch.ones(1, 8, device=DEV), torch.zeros(1, 8, device=DEV)
+    for eps in (1e-6, 1e-5, 0.0):
+        y, _ = rmsn.qk_norm_rope_fwd(x.to(DEV), x.to(DEV), torch.ones(D, device=DEV), torch.ones(D, device=DEV), one,
+                                     zero, torch.zeros(T, dtype=torch.int64, device=DEV), eps)
+        m = v * v * (1.0 / D) + torch.tensor(eps, dtype=F32)
+        ref = v * (1.0 / m.sqrt())
+        normal = m > 1e-30
+        assert torch.equal(y.cpu()[..., 3][normal], ref[normal])
+
+
 def test_long_sum_of_weight_gradients():
     """Many rows into the 64 columns of dw: the bound does not grow with their number."""
     q, k, gq, gk, wq, wk, cos, sin, pos = make(None, 6000, 24, 3, 64, 64, BF16, F32, "dense", seed=5)
