@@ -198,20 +198,32 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 }
 
 
-// Shared memory of a CTA.  A warp's sums at the end of an item take the place of its own ring,
-// which is empty then; dims are in the order of the fragments (dim_of), which keeps the stores
-// free of bank conflicts.
+// A CTA's piece of an item: units [k0, k1) of a (query block, kv head) of a sequence.
+struct Piece {
+    Seq s;
+    int b, qb, h, k0, k1;
+    int64_t seq_first, u;  // first place of the sequence; first place behind the item
+};
+
+// Shared memory of a CTA.  A warp's sums at the end of an item take the place of the last stages
+// of its own ring, which is empty then; the first P stages are already filled for the next item
+// meanwhile.  Dims are in the order of the fragments (dim_of), which keeps the stores free of bank
+// conflicts.
 template <int D, int NT>
 struct Smem {
     static constexpr int S = stages_of(D);
     static constexpr int QC = 8 * NT;
-    static constexpr int OS = D + 4;  // padded row of the sums
-    union PerWarp {
-        uint8_t ring[S][2 * 20 * D];
-        float o[QC][OS];
-    } w[kWarps];
+    static constexpr int OS = D + 4;           // padded row of the sums
+    static constexpr int kStage = 2 * 20 * D;  // bytes
+    static constexpr int P = S - (QC * OS * 4 + kStage - 1) / kStage;
+    static_assert(P >= 0, "the sums fit the ring");
+    uint8_t ring[kWarps][S][kStage];
     float m[kWarps][QC], l[kWarps][QC];
     uint64_t full[kWarps][S];
+    Piece piece[kWarps];
+    __device__ __forceinline__ float* sums(int w, int col) {
+        return reinterpret_cast<float*>(&ring[0][0][0] + (w * S + P) * kStage) + col * OS;
+    }
 };
 
 // First of the two dims in the n-th pair of a row of sums: pairs run over g, then over the
@@ -630,66 +642,81 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     if (report && lane == 0) a.prefix[a.seqs] = total;
     if (begin >= end) return;
 
-    Seq s = seq_of<QC>(a, b, false);
+    // Every warp's own copy of where it is, in shared memory: the registers are the sums'.
+    Piece& it = sm.piece[warp];
+    auto advance = [&](Piece p) -> bool {  // from p to the CTA's next piece, if there is one
+        bool found = false;
+        while (p.u < end && !found) {
+            while (p.u >= p.seq_first + places_of(p.s, a.kv_heads)) {
+                p.seq_first += places_of(p.s, a.kv_heads);
+                p.s = seq_of<QC>(a, ++p.b, false);  // u < total, so a sequence with work follows
+            }
+            const int64_t in_seq = p.u - p.seq_first;
+            const int len = p.s.units + kItemCost;
+            const int item =
+                in_seq >> 32 ? (int)(in_seq / len) : (int)((uint32_t)in_seq / (uint32_t)len);
+            const int64_t first = p.seq_first + (int64_t)item * len + kItemCost;  // of its units
+            p.k0 = (int)max(p.u - first, (int64_t)0);
+            p.k1 = (int)min((int64_t)p.s.units, end - first);
+            p.u = first + p.s.units;
+            p.qb = item / a.kv_heads;
+            p.h = item - p.qb * a.kv_heads;
+            found = p.k1 > p.k0;
+        }
+        __syncwarp();  // every lane has read it
+        if (lane == 0) it = p;
+        __syncwarp();
+        return found;
+    };
     uint32_t phase = 0u, have = 0u;  // per stage: parity waited for next; records in flight
     bool dead = false;
-    Warp<D, NT> st;
-
-    for (int64_t u = begin; u < end;) {
-        while (u >= seq_first + places_of(s, a.kv_heads)) {
-            seq_first += places_of(s, a.kv_heads);
-            s = seq_of<QC>(a, ++b, false);  // u < total, so a sequence with work follows
+    // record x & 1 of this warp's unit x / 2; -1: behind the end, or page outside the cache
+    auto record = [&](int x) -> int {
+        const int ku = it.k0 + warp + (x >> 1) * kWarps, kb = 2 * ku + (x & 1);
+        if (ku >= it.k1 || kb * kKv4Block >= it.s.len) return -1;
+        const int p = kb / a.nb;
+        const int page = __ldg(a.table + it.b * a.table_stride + p);
+        if (page < 0 || page >= a.pages) {
+            atomicOr(a.err, ERR_INDEX);
+            return -1;
         }
-        const int64_t in_seq = u - seq_first;
-        const int len = s.units + kItemCost;
-        const int item = in_seq >> 32 ? (int)(in_seq / len) : (int)((uint32_t)in_seq / (uint32_t)len);
-        const int64_t first = seq_first + (int64_t)item * len + kItemCost;  // place of unit 0
-        const int k0 = (int)max(u - first, (int64_t)0);
-        const int k1 = (int)min((int64_t)s.units, end - first);
-        u = first + s.units;
-        if (k1 <= k0) continue;
-        const int qb = item / a.kv_heads, h = item - qb * a.kv_heads;
-        // every column sees the tokens before this one
-        const int safe = s.len - s.n + 1 + a.over_group(qb * QC);
+        return (page * a.kv_heads + it.h) * a.nb + (kb - p * a.nb);
+    };
+    // copies unit x's records (rec of this lane's window) to a stage; which ones there are
+    auto issue = [&](int stage, int window, int x) {
+        const int r0 = __shfl_sync(0xffffffffu, window, 2 * x & 31);
+        const int r1 = __shfl_sync(0xffffffffu, window, (2 * x + 1) & 31);
+        const uint32_t got = (r0 >= 0 ? 1u : 0u) | (r1 >= 0 ? 2u : 0u);
+        have = (have & ~(3u << (2 * stage))) | got << (2 * stage);
+        if (lane == 0 && got) {
+            uint64_t* bar = &sm.full[warp][stage];
+            uint8_t* dst = sm.ring[warp][stage];
+            mbar_arrive_expect_tx(bar, got == 3u ? 2 * kRec : kRec);
+            if (got == 3u && r1 == r0 + 1) {
+                bulk_load(dst, a.cache + (int64_t)r0 * kRec, 2 * kRec, bar);
+            } else {
+                if (r0 >= 0) bulk_load(dst, a.cache + (int64_t)r0 * kRec, kRec, bar);
+                if (r1 >= 0) bulk_load(dst + kRec, a.cache + (int64_t)r1 * kRec, kRec, bar);
+            }
+        }
+    };
+    auto units_of = [&]() {
+        return dead ? 0 : max(0, (it.k1 - it.k0 - warp + kWarps - 1) / kWarps);
+    };
 
-        // record x & 1 of this warp's unit x / 2; -1: behind the end, or page outside the cache
-        const int records = (s.len + kKv4Block - 1) / kKv4Block;
-        auto record = [&](int x) -> int {
-            const int ku = k0 + warp + (x >> 1) * kWarps, kb = 2 * ku + (x & 1);
-            if (ku >= k1 || kb >= records) return -1;
-            const int p = kb / a.nb;
-            const int page = __ldg(a.table + b * a.table_stride + p);
-            if (page < 0 || page >= a.pages) {
-                atomicOr(a.err, ERR_INDEX);
-                return -1;
-            }
-            return (page * a.kv_heads + h) * a.nb + (kb - p * a.nb);
-        };
-        // copies unit x's records (rec of this lane's window) to a stage; which ones there are
-        auto issue = [&](int stage, int window, int x) {
-            const int r0 = __shfl_sync(0xffffffffu, window, 2 * x & 31);
-            const int r1 = __shfl_sync(0xffffffffu, window, (2 * x + 1) & 31);
-            const uint32_t got = (r0 >= 0 ? 1u : 0u) | (r1 >= 0 ? 2u : 0u);
-            have = (have & ~(3u << (2 * stage))) | got << (2 * stage);
-            if (lane == 0 && got) {
-                uint64_t* bar = &sm.full[warp][stage];
-                uint8_t* dst = sm.w[warp].ring[stage];
-                mbar_arrive_expect_tx(bar, got == 3u ? 2 * kRec : kRec);
-                if (got == 3u && r1 == r0 + 1) {
-                    bulk_load(dst, a.cache + (int64_t)r0 * kRec, 2 * kRec, bar);
-                } else {
-                    if (r0 >= 0) bulk_load(dst, a.cache + (int64_t)r0 * kRec, kRec, bar);
-                    if (r1 >= 0) bulk_load(dst + kRec, a.cache + (int64_t)r1 * kRec, kRec, bar);
-                }
-            }
-        };
-        const int n = dead ? 0 : max(0, (k1 - k0 - warp + kWarps - 1) / kWarps);
-        int now = record(lane), next = record(32 + lane);
+    if (!advance(Piece{seq_of<QC>(a, b, false), b, 0, 0, 0, 0, seq_first, begin})) return;
+    int now = record(lane), next = record(32 + lane), n = units_of();
 #pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (i < n) issue(i, now, i);
-        st.begin(a, s, qb, h, lane);
-        int stage = 0;
+    for (int i = 0; i < S; ++i)
+        if (i < n) issue(i, now, i);
+    Warp<D, NT> st;
+    for (;;) {
+        const Seq s = it.s;
+        const int len = s.len;
+        // every column sees the tokens before this one
+        const int safe = len - s.n + 1 + a.over_group(it.qb * QC);
+        st.begin(a, s, it.qb, it.h, lane);
+        int stage = 0, tok0 = (it.k0 + warp) * kUnit;
         for (int i = 0; i < n; ++i) {
             const int got = (have >> (2 * stage)) & 3u;
             if (got) {
@@ -702,11 +729,10 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 }
                 phase ^= 1u << stage;
                 have &= ~(3u << (2 * stage));
-                const int tok0 = (k0 + warp + i * kWarps) * kUnit;
                 if (got == 3 && tok0 + kUnit <= safe)
-                    st.template unit<true>(a, sm.w[warp].ring[stage], tok0, s.len, got, lane);
+                    st.template unit<true>(a, sm.ring[warp][stage], tok0, len, got, lane);
                 else
-                    st.template unit<false>(a, sm.w[warp].ring[stage], tok0, s.len, got, lane);
+                    st.template unit<false>(a, sm.ring[warp][stage], tok0, len, got, lane);
                 __syncwarp();
             }
             const int ahead = i + S;
@@ -716,6 +742,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 next = record(2 * (i + 17) + lane);
             }
             stage = stage + 1 == S ? 0 : stage + 1;
+            tok0 += kWarps * kUnit;
         }
 
         // merge the warps
@@ -736,17 +763,29 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    *reinterpret_cast<float2*>(&sm.w[warp].o[col][16 * i + 2 * g]) =
+                    *reinterpret_cast<float2*>(sm.sums(warp, col) + 16 * i + 2 * g) =
                         make_float2(st.o[nt][i][c] * pk, st.o[nt][i][c + 2] * pk);
             }
         }
+        const bool whole = it.k0 == 0 && it.k1 == it.s.units;
+        const int slot = it.u - it.s.units < begin ? 0 : 1;
+        const int col0 = it.qb * QC, cols = it.s.n * a.group, head0 = it.h * a.group, q0 = it.s.q0;
+
+        // the next piece's first units are on their way while this one's warps merge
+        const bool more = it.u < end && advance(it);
+        if (more) {
+            now = record(lane);
+            next = record(32 + lane);
+            n = units_of();
+#pragma unroll
+            for (int i = 0; i < Sm::P; ++i)
+                if (i < n) issue(i, now, i);
+        }
         __syncthreads();
-        const bool whole = k0 == 0 && k1 == s.units;
-        const int slot = first < begin ? 0 : 1;
         for (int x = threadIdx.x; x < QC * D / 4; x += kWarps * 32) {
-            const int col = x / (D / 4), n = x % (D / 4);
-            const int idx = qb * QC + col;
-            if (idx >= s.n * a.group) continue;
+            const int col = x / (D / 4), e4 = x % (D / 4);
+            const int idx = col0 + col;
+            if (idx >= cols) continue;
             float m = sm.m[0][col];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm.m[w][col]);
@@ -755,7 +794,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float e = ex2(sm.m[w][col] - m);
-                const float4 o = *reinterpret_cast<const float4*>(&sm.w[w].o[col][4 * n]);
+                const float4 o = *reinterpret_cast<const float4*>(sm.sums(w, col) + 4 * e4);
                 l = fmaf(e, sm.l[w][col], l);
                 v.x = fmaf(e, o.x, v.x);
                 v.y = fmaf(e, o.y, v.y);
@@ -763,18 +802,22 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 v.w = fmaf(e, o.w, v.w);
             }
             if (whole) {
-                const int i = a.over_group(idx), hq = h * a.group + idx - i * a.group;
-                const int64_t row = s.q0 + i;
+                const int i = a.over_group(idx), hq = head0 + idx - i * a.group;
+                const int64_t row = q0 + i;
                 put_row<D>(a.out + row * a.out_st + hq * a.out_sh,
-                           a.lse ? a.lse + row * a.heads + hq : nullptr, n, v, m, l);
+                           a.lse ? a.lse + row * a.heads + hq : nullptr, e4, v, m, l);
             } else {
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * QC + col;
-                *reinterpret_cast<float4*>(a.part + at * D + 4 * n) = v;
-                if (n == 0) a.part_ml[at] = make_float2(m, l);
+                *reinterpret_cast<float4*>(a.part + at * D + 4 * e4) = v;
+                if (e4 == 0) a.part_ml[at] = make_float2(m, l);
             }
         }
+        if (!more) break;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is next
         __syncthreads();
+#pragma unroll
+        for (int i = Sm::P; i < S; ++i)
+            if (i < n) issue(i, now, i);
     }
     // after a wait that ran out: the copies still in flight must land before the CTA ends
     for (int i = 0; i < S; ++i)
