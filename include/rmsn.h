@@ -1,7 +1,8 @@
 /*
  * rmsn.h -- C ABI of the GB300 (sm_103a) RMSNorm library.
  *
- * Three operations, each enqueued on a caller-provided CUDA stream:
+ * Three operations on whole rows, each enqueued on a caller-provided CUDA stream (the norms
+ * inside attention, with a 4-bit cache, are described in their own section below):
  *
  *   rmsnorm_fwd                        y = x * rstd * w,  rstd = 1/sqrt(mean(x^2) + eps)
  *   rmsnorm_bwd                        dx = rstd * (g - xhat * mean(g * xhat)),
@@ -472,7 +473,7 @@ typedef struct {
  * is stored as it is.  All in bf16; B = 1 (tokens [T, heads, D] by strides).
  *
  *   slots  [T] where each token's K and V go.  A token with a negative slot is padding: nothing
- *          is read or written for it, q_out included.  A slot beyond the cache, or a position
+ *          is written for it, q_out included.  A slot beyond the cache, or a position
  *          that is not a table row: likewise, and bit 3 is set.  Two tokens with one slot in a
  *          call leave that slot with an unspecified mixture of both.
  *   q_out  may be q itself.
@@ -504,7 +505,7 @@ int kv4_read(const rmsn_kv4_t* cache, const int64_t* slots, const rmsn_heads_t* 
  *             head i reads kv head i / (heads / kv_heads)); out must not overlap q
  *   lse       [T, heads] fp32, contiguous, or NULL
  *   page_table  int32 [seqs, table_width], rows table_stride apart; entries behind a
- *             sequence's length are not read
+ *             sequence's length are not read; table_width * page_size is at most 2^30
  *   kv_lens   int32 [seqs]; less than 0 counts as 0, more than table_width * page_size as that
  *             (and sets bit 3)
  *   cu_q      int32 [seqs + 1], rising, within 0 .. T; rows of out and lse that no sequence
@@ -513,6 +514,8 @@ int kv4_read(const rmsn_kv4_t* cache, const int64_t* slots, const rmsn_heads_t* 
  *             are worked on together; results are right for any value.
  *   workspace at least kv4_attention_workspace_bytes(seqs, D, device) bytes, 16-byte aligned;
  *             contents do not matter.  Calls that may overlap in time need one each.
+ * Ranges: |scale q| below 2^117 in a row (beyond it the row's result means nothing) and its
+ * largest |q| from 2^-85 (below, q loses bits); values of V below 2^-100 may count as 0.
  * A page id outside the cache: its tokens are left out and bit 3 is set.  What a cached token
  * holds reaches only the queries that see it, NaN included.  The work split, and so the
  * rounding, depends on all lengths of the call; the same call gives the same bits every time.

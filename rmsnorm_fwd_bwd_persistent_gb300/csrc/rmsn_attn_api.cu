@@ -294,11 +294,12 @@ int kv4_attention(const rmsn_heads_t* q, const rmsn_kv4_t* cache, const int32_t*
     RMSN_CHECK(check_heads(q, 1, T, D, RMSN_BF16, false, &hq));
     RMSN_CHECK(check_heads(out, 1, T, D, RMSN_BF16, true, &ho));
     if (table_width < 0 || table_stride < table_width) return RMSN_ERR_INVALID_ARG;
-    if (table_width > most / cache->page_size || table_stride > kMaxStride)
+    // token indexes past a sequence's end (partial units, columns) stay in 32 bits
+    if (table_width > ((int64_t)1 << 30) / cache->page_size || table_stride > kMaxStride)
         return RMSN_ERR_UNSUPPORTED_SHAPE;
     if (!cu_q && T != seqs) return RMSN_ERR_INVALID_ARG;
     // (query token, head) columns and all units of the work split stay in range
-    if (T > most / q->heads) return RMSN_ERR_UNSUPPORTED_SHAPE;
+    if (T > (most - 1024) / q->heads) return RMSN_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || seqs == 0) return RMSN_OK;
     if (!kv_lens || (!page_table && table_width > 0)) return RMSN_ERR_INVALID_ARG;
     if (!aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))

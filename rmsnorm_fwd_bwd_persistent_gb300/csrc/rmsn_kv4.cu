@@ -294,8 +294,9 @@ struct AppendSmem {
 
 // The same for many tokens: persistent, with CTAs for q, for k and for v, each warp streaming the
 // rows of its units.  Measured with 32 + 8 + 8 heads of 128: at 16384 tokens (with the read that
-// follows) 111.5 us with the kernel above, 97.8 so; at 64 tokens, where there is nothing to run
-// ahead of, 7.6 and 8.5.
+// follows) 111.5 us with the kernel above, 93 so; at 64 tokens, where there is nothing to run
+// ahead of, 7.6 and 8.5.  With the read that is 57% of the
+// copy rate at 4096 tokens, 72% at 16384; 56% of the issue slots are in use.
 template <int LPR, bool NB>
 __global__ void __launch_bounds__(kWarps * 32) kv4_append_stream_kernel(const AppendArgs a) {
     constexpr int RPW = 32 / LPR, D = 16 * LPR, S = kAppendStages;
@@ -430,8 +431,8 @@ struct ReadArgs {
 // Lanes per row D/64: a lane takes 64 dims of K and 64 of V, which are 32 bytes of codes each (K:
 // the 16 dims 16 h .. of four groups, two words each; V: neighbours), so it loads six 16-byte
 // pieces and writes eight of 32 bytes, whole sectors.  Measured at 32768 tokens of 8 heads of 128
-// (floor 26 us): 42 us with 16 dims per lane, ten loads of 2 to 4 bytes and four times the lanes'
-// instructions.
+// (floor 26 us): 29.7 us, 92% of the copy rate at 65536; 42 us with 16 dims per lane, ten loads of 2
+// to 4 bytes and four times the lanes' instructions.
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a) {
     constexpr int LN = D / 64, RPW = 32 / LN;
@@ -505,20 +506,18 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_read_kernel(const ReadArgs a)
     }
 }
 
-// Shares `all` CTAs of `warps` warps out to `sides` tensors by their work: a unit's chunks, and
-// `enter` chunks' time for entering it, times the tensor's own factor.
-void share_ctas(int64_t all, int warps, int sides, const Span* sp, const int64_t* units,
-                       const double* factor, double enter, int* grid) {
-    double work[3] = {0, 0, 0}, sum = 0;
-    for (int i = 0; i < sides; ++i) {
-        work[i] = (double)units[i] * (sp[i].per_part * factor[i] + enter);
+// Shares the append's CTAs out to q, k and v by their work: a unit's chunks (norm and rotation; both
+// and the quantiser; the quantiser alone), and one and a half chunks' time for entering it.
+void share_ctas(int64_t all, const Span (&sp)[3], const int64_t (&units)[3], int (&grid)[3]) {
+    const double factor[3] = {1, 1.8, 1.2};
+    double work[3], sum = 0;
+    for (int i = 0; i < 3; ++i) {
+        work[i] = (double)units[i] * (sp[i].per_part * factor[i] + 1.5);
         sum += work[i];
     }
-    for (int i = 0; i < sides; ++i) {
-        int64_t g = (int64_t)((double)all * work[i] / sum + 0.5);
-        const int64_t need = (units[i] + warps - 1) / warps;
-        g = g < 1 ? 1 : g;
-        grid[i] = (int)(need < g ? need : g);
+    for (int i = 0; i < 3; ++i) {
+        const int64_t g = std::max<int64_t>(1, (int64_t)((double)all * work[i] / sum + 0.5));
+        grid[i] = (int)std::min(g, (units[i] + kWarps - 1) / kWarps);
     }
 }
 
@@ -564,9 +563,7 @@ cudaError_t run_append(const Kv4Append& c, cudaStream_t s) {
     auto kernel = kv4_append_stream_kernel<LPR, NB>;
     cudaError_t e = fit_grid((const void*)kernel, L, kWarps * 32, &all);
     if (e != cudaSuccess) return e;
-    // norm and rotation, both and the quantiser, the quantiser alone
-    const double factor[3] = {1, 1.8, 1.2};
-    share_ctas(all, kWarps, 3, a.span, units, factor, 1.5, a.grid);
+    share_ctas(all, a.span, units, a.grid);
     kernel<<<a.grid[0] + a.grid[1] + a.grid[2], kWarps * 32, (size_t)L.smem, s>>>(a);
     return cudaGetLastError();
 }

@@ -31,10 +31,19 @@
 // with kItemCost places before its units for what entering and merging it costs; the line is cut
 // into equal shares, one per CTA, so ragged batches and single long sequences load all SMs
 // alike.  (Without those places CTAs that got many short items were late: 64 sequences of up to
-// 500 tokens took 35 us, 16 of up to 2000, the same tokens, 16.)  A CTA's four warps take the units of an item in turn, each streaming its own through
-// a ring in shared memory (bulk copies of whole records), and merge at the item's end.  An item
-// that lies in several CTAs leaves partial sums in the workspace, which kv4_combine_kernel adds
-// in CTA order: results do not depend on timing.
+// 500 tokens took 35 us, 16 of up to 2000, the same tokens, 16.)  A CTA's four warps take the
+// units of an item in turn, each streaming its own through a ring in shared memory (bulk copies of
+// whole records), and merge at the item's end, while the next item's first units are copied.  An
+// item that lies in several CTAs leaves partial sums in the workspace, which kv4_combine_kernel
+// adds in CTA order: results do not depend on timing.
+//
+// Measured on GB300, 32 + 8 heads of 128, replayed from a graph: one sequence of 131072 tokens
+// 40.7 us (floor 24.7), 64 sequences of 500 to 16000 122 us (floor 100); longer caches add 93% of
+// the copy rate.  What is left of a call is 8 to 11 us for its launches, the first copies, the merges
+// and the combine; while it streams, 57% of the issue slots and 53% of the logic pipe are in use
+// and the matrix pipe is at 23%.  Tried and not kept: units split finer at the ends of shares, one
+// CTA per SM (drafts 22 -> 37 us), a dependent launch announced before the end (no change).
+#include <algorithm>
 #include <cfloat>
 
 #include "rmsn_internal.h"
@@ -333,7 +342,7 @@ struct Warp {
                 qz[nt][NZ - 1][0] = term[2];
                 qz[nt][NZ - 1][1] = 0u;
             }
-            const float fac = a.scale_log2 * pow2(ex + 24);
+            const float fac = a.scale_log2 * 16777216.f * pow2(ex);  // 2^(ex + 24) may leave FP32
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 f[nt][c] = __shfl_sync(0xffffffffu, fac, 8 * t + 4 * c);  // of column 2t + c
@@ -979,7 +988,8 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     if (e != cudaSuccess) return e;
 
     // an item lies in about grid / items CTAs (all of the same length): from 8 on, a CTA per row
-    const int64_t rows = (int64_t)c.tokens * c.heads, items = (int64_t)c.seqs * c.kv_heads;
+    const int64_t rows = (int64_t)c.tokens * c.heads;
+    const int64_t items = std::max((int64_t)c.seqs * c.kv_heads, rows / (8 * NT));
     const bool wide = grid >= 8 * items;
     const int per_cta = wide ? 1 : combine_threads(false) * 4 / D;
     cudaLaunchConfig_t cfg = {};

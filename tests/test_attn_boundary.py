@@ -143,7 +143,9 @@ def test_attention_refusals(lib):
     for s in (float("nan"), float("inf")):
         assert att(scale=s) == INVALID
     assert att(stride=2) == INVALID and att(width=-1) == INVALID
-    assert att(width=1 << 30, stride=1 << 30) == SHAPE           # longer than 2^31 tokens
+    assert att(width=1 << 30, stride=1 << 30) == SHAPE           # longer than 2^30 tokens
+    assert att(width=(1 << 25) + 1, stride=1 << 30) == SHAPE     # the shortest such table
+    assert att(T=1 << 29) == SHAPE                               # 2^31 (token, head) columns
     assert att(table=None) == INVALID and att(lens=None) == INVALID
     assert att(lens=A + 2) == MISALIGNED and att(cu=A + 1) == MISALIGNED and att(lse=A + 2) == MISALIGNED
     assert att(ws=None, n=0) == WS_SMALL and att(ws=A + 8) == MISALIGNED

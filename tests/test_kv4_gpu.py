@@ -319,6 +319,21 @@ def test_score_ranges(std, scale):
     check(q, cache, table, lens, scale=scale, rms=False)
 
 
+def test_queries_near_the_ends_of_the_range():
+    """Large queries over small keys and the other way round: the scores are ordinary, the
+    factors between them (2^(exponent + 24)) are not.  The scale is a power of two, so every
+    product is that of the ordinary case, and K's codes are the same."""
+    for e in (118, 80, -70):
+        cache, table, g = filled([300, 40], 2, 32, 128, seed=5, std=1.0)
+        half = cache.view(BF16)
+        for t in range(cache.shape[0] * cache.shape[2] * 16):
+            rec = half[t // 32, :, t // 16 % 2]
+            at = R.tables(128)[0][2][t % 16].flatten()
+            rec[:, at] = rec[:, at] * 2.0 ** -e
+        q = torch.randn(2, 8, 128, generator=g).to(BF16)
+        check((q.float() * 2.0 ** e).to(BF16), cache, table, [300, 40])
+
+
 def test_rising_scores():
     """Keys that grow along the sequence: the running maximum moves all the time."""
     lens = [640]
