@@ -284,7 +284,7 @@ struct RowStream {
     }
 };
 
-constexpr int kAppendStages = 6;  // 6 KiB per warp
+constexpr int kAppendStages = 4;  // 4 KiB per warp
 constexpr int kStreamFrom = 4;    // units per warp from which the streaming kernel is taken
 
 struct AppendSmem {

@@ -40,10 +40,13 @@ struct FwdArgs {
 
 // One unit of work per warp: tpw tokens and the chunks [part * per_part, ...) of their heads.
 // blockIdx.y picks q or k and the part, blockIdx.x and the warp the tokens.
-template <typename T, int LPR, bool NB>
-__global__ void __launch_bounds__(kWarps * 32, 5) qk_fwd_kernel(const FwdArgs a) {
+// U chunks are in flight: up to 4 KiB of rows per warp as far as a unit has them; units of one or
+// two chunks (few heads) take fewer registers and more CTAs instead (T = 8192 with 4 + 4 heads of
+// 128 12.7 -> 9.9 us, with 1 + 1 4.7 -> 3.7).
+template <typename T, int LPR, bool NB, int U>
+__global__ void __launch_bounds__(kWarps * 32, U == 1 ? 7 : U == 2 && sizeof(T) == 2 ? 6 : 5)
+    qk_fwd_kernel(const FwdArgs a) {
     constexpr int RPW = 32 / LPR;
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // chunks in flight: 4 KiB of rows per warp
     const int side = blockIdx.y < a.span[0].parts ? 0 : 1;
     const Span sp = a.span[side];
     const int part = blockIdx.y - (side ? a.span[0].parts : 0);
@@ -121,10 +124,10 @@ struct BwdArgs {
 // LPR lanes has LPR * 16 elements' room), and every lane's (high, low) sums.
 template <typename T>
 struct BwdSmem {
-    static constexpr int S = sizeof(T) == 2 ? 5 : 3;  // 10 and 12 KiB per warp
+    static constexpr int S = sizeof(T) == 2 ? 4 : 3;  // 8 and 12 KiB per warp
     union {
         T ring[kWarps][S][2][512];
-        float merge[kWarps][2][256];
+        float merge[8][2][64];  // of heads of at most 64
     };
     ulonglong2 sums[2][4][kWarps * 32];  // high, low: four pairs of f2 per lane
 };
@@ -139,15 +142,20 @@ struct BwdSmem {
 // lanes are merged in a fixed order and written to the workspace, whose CTA partials
 // qk_dw_reduce_kernel adds in a fixed order.  Two-element FP32 instructions halve the arithmetic.
 //
-// Measured on GB300 with the reduce, 32 + 8 heads of 128: bf16, T = 32768 178 us, 84% of the copy
-// rate (373 us with register loads, scalar arithmetic and TwoSum per term); FP32, T = 8192 83 us,
-// 90% (121 us before the copies went in memory order).  Few or short heads leave chunks too little
-// work for what entering them costs: 4 + 4 heads 35%, heads of 64 57%.
+// Measured on GB300 with the reduce, 32 + 8 heads of 128: bf16, T = 8192 43.8 us, 86% of the copy
+// rate, T = 32768 165 us, 91% (373 us with register loads, scalar arithmetic and TwoSum per term);
+// FP32, T = 8192 83 us, 90% (121 us before the copies went in memory order).  The launches, the
+// first copies and the merges cost 6 us: with 4 + 4 heads of 128, T = 8192, 44%.  Merging the lanes
+// by shuffles instead of from shared memory took 1 to 2 us more.  Deeper rings are
+// slower, for DRAM's sake: bf16, T = 32768 with 4, 5, 6 and 7 stages 160, 169, 173 and 176 us.
 template <typename T, int LPR, bool NB>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kWarps * 32, 3)
     qk_bwd_kernel(const BwdArgs a) {
     using Sm = BwdSmem<T>;
     constexpr int RPW = 32 / LPR, S = Sm::S, E = 16 / sizeof(T);
+    // A unit's angles are loaded while the unit before it is worked on, its position one more
+    // ahead; the FP32 kernel has no registers left for that.
+    constexpr bool AHEAD = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     Sm& sm = *reinterpret_cast<Sm*>(smem_raw);
     asm volatile("griddepcontrol.launch_dependents;");  // the reduce waits for this grid's end
@@ -244,20 +252,47 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             acc[2 * i] = acc[2 * i + 1] = 0ull;
         }
     };
-    int stage = 0, added = 0;
-    for (At at{(int64_t)cta * kWarps + warp, 0, 0, 0}; at.unit < units; at.unit += stride) {
-        enter(at);
-        const Token tk = find_token(at.tok, a.tokens, a.T, a.rope, a.err,
-                                    side == 0 && at.c == 0 && l == 0 && hsub == 0);
-        const bool ok = tk.ok && dims_ok;
-        Angles ang;
+    auto position = [&](const At& at) -> int64_t {
+        const int t = at.tok < a.tokens ? at.tok : 0, b = a.tokens == a.T ? 0 : t / a.T;
+        return at.unit < units ? __ldg(a.rope.pos + b * a.rope.pos_sb + (t - b * a.T) * a.rope.pos_st) : 0;
+    };
+    auto turn = [&](Angles& ang, int64_t pos) {
         ang.identity();
-        if (ok && rl.turns) {
-            const int64_t p = tk.pos * (a.rope.rd / 2) + 8 * l;
+        if (rl.turns && pos >= 0 && pos < a.rope.rows) {
+            const int64_t p = pos * (a.rope.rd / 2) + 8 * l;
             ang.load(a.rope.cos + p, a.rope.sin + p);
         }
+    };
+    int stage = 0, added = 0;
+    At at{(int64_t)cta * kWarps + warp, 0, 0, 0}, nx{at.unit + stride, 0, 0, 0};
+    enter(at);
+    int64_t pos = 0, pos_nx = 0;
+    Angles ang, ang_nx;
+    if (AHEAD) {
+        enter(nx);
+        pos = position(at);
+        pos_nx = position(nx);
+        turn(ang_nx, pos);
+    }
+    while (at.unit < units) {
+        At n2{nx.unit + stride, 0, 0, 0};
+        if (!AHEAD) pos = position(at);
+        const bool there = pos >= 0 && pos < a.rope.rows;
+        const bool ok = at.tok < a.tokens && there && dims_ok;
+        if (!there && at.tok < a.tokens && side == 0 && at.c == 0 && l == 0 && hsub == 0)
+            atomicOr(a.err, ERR_INDEX);
+        if (AHEAD) {
+            ang = ang_nx;
+            turn(ang_nx, pos_nx);
+            pos = pos_nx;
+            enter(n2);
+            pos_nx = position(n2);
+        } else {
+            turn(ang, pos);
+        }
+        const int tok = at.tok < a.tokens ? at.tok : 0, bt = a.tokens == a.T ? 0 : tok / a.T;
         int h = (at.c << sp.log_hpw) + hsub;
-        T* d0 = a.dx[side].row<T>(tk.b, tk.t) + h * a.dx[side].sh;
+        T* d0 = a.dx[side].row<T>(bt, tok - bt * a.T) + h * a.dx[side].sh;
         T* d1 = d0 + rl.off1;
         d0 += rl.off0;
         if (added + at.c1 - at.c > kBlock) {
@@ -314,40 +349,48 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 4 : 3)
             d0 += step_d;
             d1 += step_d;
         }
+        at = nx;
+        if (AHEAD)
+            nx = n2;
+        else
+            nx.unit += stride, enter(at);
     }
     flush();
     copy_wait<0>();
     __syncthreads();
 
-    // merge the warp's rows (lanes of equal l), then the warps in order
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const ulonglong2 hi = sm.sums[0][i / 2][threadIdx.x], lo = sm.sums[1][i / 2][threadIdx.x];
-        const f2 hh = i & 1 ? hi.y : hi.x, ll = i & 1 ? lo.y : lo.x;
-        float h0 = f2_lo(hh), h1 = f2_hi(hh), e0 = f2_lo(ll), e1 = f2_hi(ll);
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) {
-            const float a0 = __shfl_xor_sync(0xffffffffu, h0, o), b0 = __shfl_xor_sync(0xffffffffu, e0, o);
-            const float a1 = __shfl_xor_sync(0xffffffffu, h1, o), b1 = __shfl_xor_sync(0xffffffffu, e1, o);
-            comp_merge(h0, e0, a0, b0);
-            comp_merge(h1, e1, a1, b1);
-        }
-        if (rr == 0 && dims_ok) {
-            const int col = (i < 4 ? rl.off0 : rl.off1 - 8) + 2 * i;
-            sm.merge[warp][0][col] = h0;
-            sm.merge[warp][0][col + 1] = h1;
-            sm.merge[warp][1][col] = e0;
-            sm.merge[warp][1][col + 1] = e1;
+    // Every column's sums of the CTA's 128 / LPR rows: G threads per column merge 16 rows (or 8)
+    // each in order, and their results are merged in order.
+    constexpr int G = LPR < 8 ? 8 / LPR : 1, ROWS = kWarps * 32 / LPR / G;
+    float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D;
+    const float* sums = reinterpret_cast<const float*>(sm.sums);
+    for (int x = threadIdx.x; x < 16 * LPR * G; x += kWarps * 32) {
+        const int cl = x % LPR, e = x / LPR % 16, part = x / (16 * LPR);
+        if (16 * cl >= a.D) continue;
+        const float* p = sums + ((e / 4) * kWarps * 32 + part * ROWS * LPR + cl) * 4 + e % 4;
+        constexpr int LOW = 4 * kWarps * 32 * 4;  // from a high to its low
+        float h = p[0], low = p[LOW];
+#pragma unroll 4
+        for (int r = 1; r < ROWS; ++r) comp_merge(h, low, p[r * LPR * 4], p[r * LPR * 4 + LOW]);
+        RowLane<NB> at;
+        at.init(cl, a.rope.rd);
+        const int col = e < 8 ? at.off0 + e : at.off1 + e - 8;
+        if (G == 1) {
+            out[col] = h;
+            out[a.D + col] = low;
+        } else {
+            sm.merge[part][0][col] = h;
+            sm.merge[part][1][col] = low;
         }
     }
+    if (G == 1) return;
     __syncthreads();
     for (int col = threadIdx.x; col < a.D; col += kWarps * 32) {
-        float h = sm.merge[0][0][col], e = sm.merge[0][1][col];
+        float h = sm.merge[0][0][col], low = sm.merge[0][1][col];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) comp_merge(h, e, sm.merge[i][0][col], sm.merge[i][1][col]);
-        float* out = a.ws + (int64_t)blockIdx.x * 2 * a.D + col;
-        out[0] = h;
-        out[a.D] = e;
+        for (int i = 1; i < G; ++i) comp_merge(h, low, sm.merge[i][0][col], sm.merge[i][1][col]);
+        out[col] = h;
+        out[a.D + col] = low;
     }
 }
 
@@ -359,7 +402,7 @@ constexpr int kReduceWarps = 32;
 __global__ void __launch_bounds__(kReduceWarps * 32)
     qk_dw_reduce_kernel(const float* __restrict__ ws, float* dwq, float* dwk, int D, int gq, int gk) {
     __shared__ float sh[kReduceWarps][33], sl[kReduceWarps][33];
-    constexpr int U = 8;
+    constexpr int U = 15;  // all of a warp's partials are in flight at once
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     const int n = blockIdx.y ? gk : gq;
@@ -367,13 +410,18 @@ __global__ void __launch_bounds__(kReduceWarps * 32)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float h = 0.f, e = 0.f;
     if (col < D) {
+        const uint32_t step = 2 * kReduceWarps * D;
+        p += col;
         for (int i = warp; i < n; i += U * kReduceWarps) {
             float vh[U], vl[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int k = i + kReduceWarps * u;
-                vh[u] = k < n ? __ldcg(p + (int64_t)k * 2 * D + col) : 0.f;
-                vl[u] = k < n ? __ldcg(p + (int64_t)k * 2 * D + D + col) : 0.f;
+                const uint32_t at = (uint32_t)i * 2 * D + u * step;
+                vh[u] = vl[u] = 0.f;
+                if (i + kReduceWarps * u < n) {
+                    vh[u] = __ldcg(p + at);
+                    vl[u] = __ldcg(p + at + D);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) comp_merge(h, e, vh[u], vl[u]);
@@ -428,8 +476,15 @@ cudaError_t run_fwd(const QkCall& c, cudaStream_t s) {
     a.w_bf16 = c.w_dt;
     a.wide = rows_on_32_bytes(c.y, c.x_dt);
     a.eps = c.eps;
-    qk_fwd_kernel<T, LPR, NB>
-        <<<dim3((unsigned)gx, a.span[0].parts + a.span[1].parts), kWarps * 32, 0, s>>>(a);
+    const dim3 grid((unsigned)gx, a.span[0].parts + a.span[1].parts);
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    const int most = a.span[0].per_part > a.span[1].per_part ? a.span[0].per_part : a.span[1].per_part;
+    if (most == 1)
+        qk_fwd_kernel<T, LPR, NB, 1><<<grid, kWarps * 32, 0, s>>>(a);
+    else if (U > 2 && most == 2)
+        qk_fwd_kernel<T, LPR, NB, 2><<<grid, kWarps * 32, 0, s>>>(a);
+    else
+        qk_fwd_kernel<T, LPR, NB, U><<<grid, kWarps * 32, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -447,12 +502,13 @@ cudaError_t run_bwd(const QkCall& c, cudaStream_t s) {
         a.w[i] = c.w[i];
         a.span[i] = make_span(heads[i], RPW, per);
         units[i] = groups_of(c.tokens, a.span[i], RPW) * a.span[i].parts;
-        work[i] = units[i] * (2 * a.span[i].per_part + 3);
+        work[i] = units[i] * (2 * a.span[i].per_part + (sizeof(T) == 2 ? 2 : 3));
     }
     // The CTAs of both sides together are those that are resident at once, shared out by the
-    // work: a unit's chunks, and about one and a half chunks' time for entering it (angles,
-    // pointers, sums).  Measured with 32 + 8 heads of 128 (bf16), T = 8192 / 32768: shared out by
-    // rows 54.5 / 207 us, waiting for k's units of two chunks; by work 46.1 / 170 us.
+    // work: a unit's chunks, and about one chunk's time for entering it (pointers, sums; in FP32,
+    // where the angles are waited for, one and a half).  Measured with 32 + 8 heads of 128 (bf16), T = 4096 / 8192 / 32768: with half a chunk's time 28.1 / 47.1
+    // / 172 us, with one 27.4 / 45.5 / 167, with one and a half 29.1 / 46.7 / 164; shared out by rows
+    // it was a fifth slower, waiting for k's units of two chunks.
     Launch L{};
     L.sms = c.sms;
     L.grid = (int64_t)c.sms * kQkBwdCtasPerSm;
