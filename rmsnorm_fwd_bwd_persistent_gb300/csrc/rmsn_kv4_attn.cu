@@ -36,6 +36,10 @@
 // whole records), and merge at the item's end, while the next item's first units are copied.  An
 // item that lies in several CTAs leaves partial sums in the workspace, which kv4_combine_kernel
 // adds in CTA order: results do not depend on timing.
+// Where no sequence is longer than 512 tokens no item is split, and the combine has nothing to do;
+// it is not launched where the page table holds no more than that.  Split and whole: one sequence
+// of 16 tokens 8.7 and 6.0 us, 64 of up to 100 11.6 and 8.6, 300 of up to 500 60 and 51, but 64 of
+// up to 1000 23.0 and 23.3, of up to 2000 29.9 and 37.4.
 //
 // Measured on GB300, 32 + 8 heads of 128, replayed from a graph: one sequence of 131072 tokens
 // 40.7 us (floor 24.7), 64 sequences of 500 to 16000 122 us (floor 100); longer caches add 93% of
@@ -60,12 +64,13 @@ constexpr int kCtasPerSm = 4;      // at most (sizes the workspace)
 constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
 constexpr int kMinShare = kWarps;  // least share of a CTA: a unit for each warp
 constexpr int kItemCost = 8;  // what entering and merging an item costs, in units
+constexpr int kWholeUnits = 16;  // no item is split where no sequence is longer
 
 // Ring stages of one unit per warp (two are 160 KiB in flight per SM at D = 128 and 256), and
 // the CTAs per SM that the registers are divided among.
 __host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : 2; }
 __host__ __device__ constexpr int ctas_of(int D, int NT) {
-    return D == 256 || NT == 4 || (D == 128 && NT == 2) ? 2 : NT == 2 ? 3 : 4;
+    return D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;
 }
 
 struct Args {
@@ -117,14 +122,16 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool report) {
     return s;
 }
 
-// Places of one sequence's items on the line, and places per CTA.
-__device__ __forceinline__ int64_t places_of(const Seq& s, int kv_heads) {
-    return s.units ? (int64_t)(s.units + kItemCost) * s.qblocks * kv_heads : 0;
+// Places of one sequence's items on the line, and places per CTA.  Where no item is split
+// (`whole`), each has one place, those without tokens too.
+__device__ __forceinline__ int64_t places_of(const Seq& s, int kv_heads, bool whole) {
+    const int64_t items = (int64_t)s.qblocks * kv_heads;
+    return whole ? items : s.units ? (s.units + kItemCost) * items : 0;
 }
-__device__ __forceinline__ int64_t share_of(int64_t places, int ctas) {
+__device__ __forceinline__ int64_t share_of(int64_t places, int ctas, int least) {
     const int64_t up = places + ctas - 1;
     const int64_t per = up >> 32 ? up / ctas : (int64_t)((uint32_t)up / (uint32_t)ctas);
-    return per < kMinShare ? kMinShare : per;
+    return per < least ? least : per;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -616,22 +623,29 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     __syncthreads();  // the barriers are there
     // The length of the line, then the sequence that holds this CTA's first place: every warp
     // for itself.
-    auto seq_places = [&](int b, bool report) -> int64_t {
-        return b < a.seqs ? places_of(seq_of<QC>(a, b, report), a.kv_heads) : 0;
-    };
     const bool report = blockIdx.x == 0 && warp == 0;
-    int64_t mine = seq_places(lane, report), total = mine;
-    for (int b = lane + 32; b < a.seqs; b += 32) total += seq_places(b, report);
+    int64_t total = 0, items = 0;
+    int longest = 0;
+    for (int b = lane; b < a.seqs; b += 32) {
+        const Seq s = seq_of<QC>(a, b, report);
+        total += places_of(s, a.kv_heads, false);
+        items += places_of(s, a.kv_heads, true);
+        longest = max(longest, s.units);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const bool whole = longest <= kWholeUnits;
+    if (whole) total = items;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t per = share_of(total, gridDim.x);
+    const int64_t per = share_of(total, gridDim.x, whole ? 1 : kMinShare);
     const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
     if (begin >= end && blockIdx.x != 0) return;
     int b = 0;
     int64_t seq_first = 0;  // first place of sequence b
     int64_t before = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-        if (b0 > 0) mine = seq_places(b0 + lane, false);
+        const int64_t mine =
+            b0 + lane < a.seqs ? places_of(seq_of<QC>(a, b0 + lane, false), a.kv_heads, whole) : 0;
         int64_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -639,16 +653,16 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
             if (lane >= o) incl += v;
         }
         const int64_t excl = before + incl - mine;
-        if (report && b0 + lane < a.seqs) a.prefix[b0 + lane] = excl;
+        if (report && !whole && b0 + lane < a.seqs) a.prefix[b0 + lane] = excl;
         const unsigned hit = __ballot_sync(0xffffffffu, begin >= excl && begin < excl + mine);
         if (hit) {
             b = b0 + __ffs(hit) - 1;
             seq_first = __shfl_sync(0xffffffffu, excl, __ffs(hit) - 1);
-            if (!report) break;
+            if (!report || whole) break;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (report && lane == 0) a.prefix[a.seqs] = total;
+    if (report && lane == 0) a.prefix[a.seqs] = whole ? -1 : total;
     if (begin >= end) return;
 
     // Every warp's own copy of where it is, in shared memory: the registers are the sums'.
@@ -656,21 +670,21 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     auto advance = [&](Piece p) -> bool {  // from p to the CTA's next piece, if there is one
         bool found = false;
         while (p.u < end && !found) {
-            while (p.u >= p.seq_first + places_of(p.s, a.kv_heads)) {
-                p.seq_first += places_of(p.s, a.kv_heads);
+            while (p.u >= p.seq_first + places_of(p.s, a.kv_heads, whole)) {
+                p.seq_first += places_of(p.s, a.kv_heads, whole);
                 p.s = seq_of<QC>(a, ++p.b, false);  // u < total, so a sequence with work follows
             }
             const int64_t in_seq = p.u - p.seq_first;
-            const int len = p.s.units + kItemCost;
+            const int len = whole ? 1 : p.s.units + kItemCost;
             const int item =
                 in_seq >> 32 ? (int)(in_seq / len) : (int)((uint32_t)in_seq / (uint32_t)len);
             const int64_t first = p.seq_first + (int64_t)item * len + kItemCost;  // of its units
-            p.k0 = (int)max(p.u - first, (int64_t)0);
-            p.k1 = (int)min((int64_t)p.s.units, end - first);
-            p.u = first + p.s.units;
+            p.k0 = whole ? 0 : (int)max(p.u - first, (int64_t)0);
+            p.k1 = whole ? p.s.units : (int)min((int64_t)p.s.units, end - first);
+            p.u = whole ? p.u + 1 : first + p.s.units;
             p.qb = item / a.kv_heads;
             p.h = item - p.qb * a.kv_heads;
-            found = p.k1 > p.k0;
+            found = whole || p.k1 > p.k0;
         }
         __syncwarp();  // every lane has read it
         if (lane == 0) it = p;
@@ -776,7 +790,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                         make_float2(st.o[nt][i][c] * pk, st.o[nt][i][c + 2] * pk);
             }
         }
-        const bool whole = it.k0 == 0 && it.k1 == it.s.units;
+        const bool alone = it.k0 == 0 && it.k1 == it.s.units;
         const int slot = it.u - it.s.units < begin ? 0 : 1;
         const int col0 = it.qb * QC, cols = it.s.n * a.group, head0 = it.h * a.group, q0 = it.s.q0;
 
@@ -810,7 +824,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 v.z = fmaf(e, o.z, v.z);
                 v.w = fmaf(e, o.w, v.w);
             }
-            if (whole) {
+            if (alone) {
                 const int i = a.over_group(idx), hq = head0 + idx - i * a.group;
                 const int64_t row = q0 + i;
                 put_row<D>(a.out + row * a.out_st + hq * a.out_sh,
@@ -877,7 +891,9 @@ __global__ void __launch_bounds__(combine_threads(WIDE)) kv4_combine_kernel(cons
         }
         return;
     }
-    const int64_t per = share_of(a.prefix[a.seqs], ctas);
+    const int64_t places = a.prefix[a.seqs];
+    if (places < 0) return;  // no item was split
+    const int64_t per = share_of(places, ctas, kMinShare);
     const int64_t u0 = a.prefix[b] + ((int64_t)qb * a.kv_heads + h) * (s.units + kItemCost) + kItemCost;
     const int64_t u1 = u0 + s.units - 1;
     const bool big = ((u1 | per) >> 32) != 0;
@@ -983,13 +999,14 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     a.prefix = reinterpret_cast<int64_t*>(ws);
     a.part = reinterpret_cast<float*>(ws + prefix_bytes(c.seqs));
     a.part_ml = reinterpret_cast<float2*>(a.part + grid * 2 * 8 * NT * D);
+    const int64_t rows = (int64_t)c.tokens * c.heads;
+    const int64_t items = std::max((int64_t)c.seqs * c.kv_heads, rows / (8 * NT));
     k<<<(unsigned)grid, kWarps * 32, (size_t)L.smem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if ((int64_t)c.table_width * c.blocks_per_page * kKv4Block <= kWholeUnits * kUnit) return e;
 
     // an item lies in about grid / items CTAs (all of the same length): from 8 on, a CTA per row
-    const int64_t rows = (int64_t)c.tokens * c.heads;
-    const int64_t items = std::max((int64_t)c.seqs * c.kv_heads, rows / (8 * NT));
     const bool wide = grid >= 8 * items;
     const int per_cta = wide ? 1 : combine_threads(false) * 4 / D;
     cudaLaunchConfig_t cfg = {};

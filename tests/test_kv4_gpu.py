@@ -243,6 +243,32 @@ def test_several_tokens(Hq, Hk, D, max_q):
     check(q, cache, table, lens, cu, max_q)
 
 
+@pytest.mark.parametrize("max_q", [1, 4])
+@pytest.mark.parametrize("Hq,Hk,D", [(8, 1, 128), (12, 4, 64), (16, 4, 128), (4, 1, 256)])
+def test_several_tokens_of_long_and_short_sequences(Hq, Hk, D, max_q):
+    """Long enough that items are split over CTAs, beside short and empty sequences."""
+    lens, counts, ps = [700, 33, 4, 0, 1250, 16, 513], [4, 1, 9, 2, 3, 0, 5], 32
+    cu = [1]
+    for n in counts:
+        cu.append(cu[-1] + n)
+    cache, table, g = filled(lens, Hk, ps, D, seed=D + Hk)
+    check(torch.randn(cu[-1] + 2, Hq, D, generator=g).to(BF16), cache, table, lens, cu, max_q)
+
+
+@pytest.mark.parametrize("longest", [0, 1, 480, 512, 513, 544])
+@pytest.mark.parametrize("width", [None, 64])
+def test_around_the_length_from_which_items_are_split(longest, width):
+    """No sequence above 512 tokens, in page tables that hold more or not (without cu_q and with)."""
+    lens, ps = [longest, 40, 0, min(longest, 300)], 32
+    cache, table, g = filled(lens, 2, ps, 128, seed=longest)
+    table = table[:, :max(-(-n // ps) for n in lens)]
+    if width:
+        table = torch.cat([table, torch.full((4, width - table.shape[1]), -1, dtype=torch.int32)], 1)
+    table = table.contiguous()
+    check(torch.randn(4, 8, 128, generator=g).to(BF16), cache, table, lens)
+    check(torch.randn(10, 8, 128, generator=g).to(BF16), cache, table, lens, [1, 4, 6, 7, 9], max_q=3)
+
+
 @pytest.mark.parametrize("Hq,Hk,D,ps", [(8, 1, 128, 256), (32, 8, 128, 64), (4, 4, 64, 16), (2, 1, 256, 128)])
 def test_long_and_ragged(Hq, Hk, D, ps):
     lens = [5000, 1, 777, 2048, 0, 16, 3001]
