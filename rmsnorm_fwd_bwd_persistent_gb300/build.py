@@ -70,7 +70,7 @@ def _binding_flags() -> tuple[list[str], list[str]]:
                 "-I", INCLUDE, "-isystem", os.path.join(base, "include"),
                 "-isystem", os.path.join(cuda, "include"),
                 "-isystem", sysconfig.get_paths()["include"]]
-    link = ["-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+    link = ["-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
             "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 

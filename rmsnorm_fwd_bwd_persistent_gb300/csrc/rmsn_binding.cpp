@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -17,6 +18,7 @@
 #include <cmath>
 #include <cstdio>
 #include <initializer_list>
+#include <optional>
 #include <string>
 #include <utility>
 
@@ -134,10 +136,16 @@ rmsn_rope_t rope(const Tensor& cos, const Tensor& sin, const Tensor& pos, bool n
     return p;
 }
 
+// A new contiguous tensor beside another (straight from the allocator: the dispatcher costs as much
+// again).
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+    return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+
 // A caller's output, checked, or a new contiguous one.
 Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Tensor& like,
               const char* name, bool contiguous) {
-    if (o == Py_None) return at::empty(shape, like.options().dtype(type));
+    if (o == Py_None) return fresh(shape, type, like);
     const Tensor& t = tensor(o, name);
     device_of({{like, "the input"}, {t, name}});
     if (t.sizes() != shape || t.scalar_type() != type || (contiguous && !t.is_contiguous()))
@@ -148,7 +156,7 @@ Tensor output(PyObject* o, at::IntArrayRef shape, at::ScalarType type, const Ten
 
 Tensor scratch(PyObject* o, size_t need, const Tensor& like) {
     if (o == Py_None)
-        return at::empty({(int64_t)(need < 16 ? 16 : need)}, like.options().dtype(at::kByte));
+        return fresh({(int64_t)(need < 16 ? 16 : need)}, at::kByte, like);
     const Tensor& t = tensor(o, "workspace");
     device_of({{like, "the input"}, {t, "workspace"}});
     if (!t.is_contiguous()) throw ValueError("workspace must be contiguous");
