@@ -60,18 +60,22 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 4;      // at most (sizes the workspace)
 constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
 constexpr int kMinShare = kWarps;  // least share of a CTA: a unit for each warp
 constexpr int kItemCost = 8;  // what entering and merging an item costs, in units
 constexpr int kWholeUnits = 16;  // no item is split where no sequence is longer
 
-// Ring stages of one unit per warp (two are 160 KiB in flight per SM at D = 128 and 256), and
-// the CTAs per SM that the registers are divided among.
-__host__ __device__ constexpr int stages_of(int D) { return D == 64 ? 4 : 2; }
+// CTAs per SM that the registers are divided among, and ring stages of one unit per warp (two are
+// 160 KiB in flight per SM at D = 128 and 256 with four CTAs).
 __host__ __device__ constexpr int ctas_of(int D, int NT) {
-    return D == 256 || NT == 4 ? 2 : NT == 2 ? 3 : 4;
+    return D == 256 || NT >= 3 ? 2 : NT == 2 ? 3 : 4;
 }
+__host__ __device__ constexpr int stages_of(int D, int NT) {
+    return D == 64 ? 4 : D == 128 && NT >= 3 ? 3 : 2;
+}
+// Whether a lane's fragments of q lie in shared memory (each lane's own place, behind its warp's
+// ring) instead of registers.
+__host__ __device__ constexpr bool q_in_smem(int D, int NT) { return NT * D > 256; }
 
 struct Args {
     const bf16* q;
@@ -222,23 +226,25 @@ struct Piece {
 };
 
 // Shared memory of a CTA.  A warp's sums at the end of an item take the place of the last stages
-// of its own ring, which is empty then; the first P stages are already filled for the next item
+// of its own ring, which is empty then, and of its q; the first P stages are already filled for the next item
 // meanwhile.  Dims are in the order of the fragments (dim_of), which keeps the stores free of bank
 // conflicts.
 template <int D, int NT>
 struct Smem {
-    static constexpr int S = stages_of(D);
+    static constexpr int S = stages_of(D, NT);
     static constexpr int QC = 8 * NT;
     static constexpr int OS = D + 4;           // padded row of the sums
     static constexpr int kStage = 2 * 20 * D;  // bytes
-    static constexpr int P = S - (QC * OS * 4 + kStage - 1) / kStage;
-    static_assert(P >= 0, "the sums fit the ring");
-    uint8_t ring[kWarps][S][kStage];
+    static constexpr int kQ = q_in_smem(D, NT) ? NT * (D / 32) * 512 : 0;
+    static constexpr int kRoom = S * kStage + kQ;  // of a warp: its ring and its fragments of q
+    static constexpr int P = (kRoom - QC * OS * 4) / kStage;
+    static_assert(kRoom >= QC * OS * 4, "the sums fit");
+    uint8_t room[kWarps][kRoom];
     float m[kWarps][QC], l[kWarps][QC];
     uint64_t full[kWarps][S];
     Piece piece[kWarps];
     __device__ __forceinline__ float* sums(int w, int col) {
-        return reinterpret_cast<float*>(&ring[0][0][0] + (w * S + P) * kStage) + col * OS;
+        return reinterpret_cast<float*>(room[w] + P * kStage) + col * OS;
     }
 };
 
@@ -266,7 +272,9 @@ struct Warp {
     static constexpr int VW = D / 64;   // V words per lane and token
     static constexpr int MT = D / 16;   // M tiles of O^T
     static constexpr int NZ = D == 256 ? 2 : 1;  // matrix steps of the minima
-    uint32_t qf[NT][NG][4];             // q as binary16 pairs, column g
+    static constexpr bool QS = q_in_smem(D, NT);
+    uint32_t qf[QS ? 1 : NT][NG][4];    // q as binary16 pairs, column g
+    uint4* qs;                          // the same in shared memory
     uint32_t qz[NT][NZ][2];             // sums of q per group, three bf16 terms, column g
     float f[NT][2];                     // factor of the code products, log2 units
     int col0, cols, seen0;              // the item's first column, all columns, tokens column 0 sees
@@ -319,8 +327,9 @@ struct Warp {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float p = e & 1 ? p1 : p0;
-                    qf[nt][j][e] = pack_f16x2(x[j][e] * p, x[j][e + 4] * p);
+                    qf[QS ? 0 : nt][j][e] = pack_f16x2(x[j][e] * p, x[j][e + 4] * p);
                 }
+                if (QS) qs[(nt * NG + j) * 32] = make_uint4(qf[0][j][0], qf[0][j][1], qf[0][j][2], qf[0][j][3]);
             }
             // the lane's two groups of the minima's product, each sum as three bf16 terms
             float u0 = z[0], u1 = z[1];
@@ -422,8 +431,11 @@ struct Warp {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float d[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(d, k0[j] & lo, k1[j] & lo, k0[j] & up, k1[j] & up, qf[nt][j][0], qf[nt][j][1]);
-                mma_f16(d, h0 & lo, h1 & lo, h0 & up, h1 & up, qf[nt][j][2], qf[nt][j][3]);
+                const uint4 q = QS ? qs[(nt * NG + j) * 32]
+                                   : make_uint4(qf[QS ? 0 : nt][j][0], qf[QS ? 0 : nt][j][1],
+                                                qf[QS ? 0 : nt][j][2], qf[QS ? 0 : nt][j][3]);
+                mma_f16(d, k0[j] & lo, k1[j] & lo, k0[j] & up, k1[j] & up, q.x, q.y);
+                mma_f16(d, h0 & lo, h1 & lo, h0 & up, h1 & up, q.z, q.w);
                 sc[nt][0] = fmaf(f0, d[0], sc[nt][0]);
                 sc[nt][1] = fmaf(f0, d[1], sc[nt][1]);
                 sc[nt][2] = fmaf(f1, d[2], sc[nt][2]);
@@ -713,7 +725,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         have = (have & ~(3u << (2 * stage))) | got << (2 * stage);
         if (lane == 0 && got) {
             uint64_t* bar = &sm.full[warp][stage];
-            uint8_t* dst = sm.ring[warp][stage];
+            uint8_t* dst = sm.room[warp] + stage * Sm::kStage;
             mbar_arrive_expect_tx(bar, got == 3u ? 2 * kRec : kRec);
             if (got == 3u && r1 == r0 + 1) {
                 bulk_load(dst, a.cache + (int64_t)r0 * kRec, 2 * kRec, bar);
@@ -733,6 +745,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     for (int i = 0; i < S; ++i)
         if (i < n) issue(i, now, i);
     Warp<D, NT> st;
+    st.qs = reinterpret_cast<uint4*>(sm.room[warp] + S * Sm::kStage) + lane;
     for (;;) {
         const Seq s = it.s;
         const int len = s.len;
@@ -753,9 +766,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 phase ^= 1u << stage;
                 have &= ~(3u << (2 * stage));
                 if (got == 3 && tok0 + kUnit <= safe)
-                    st.template unit<true>(a, sm.ring[warp][stage], tok0, len, got, lane);
+                    st.template unit<true>(a, sm.room[warp] + stage * Sm::kStage, tok0, len, got, lane);
                 else
-                    st.template unit<false>(a, sm.ring[warp][stage], tok0, len, got, lane);
+                    st.template unit<false>(a, sm.room[warp] + stage * Sm::kStage, tok0, len, got, lane);
                 __syncwarp();
             }
             const int ahead = i + S;
@@ -956,8 +969,16 @@ __global__ void __launch_bounds__(combine_threads(WIDE)) kv4_combine_kernel(cons
 
 int64_t prefix_bytes(int seqs) { return ((int64_t)(seqs + 1) * 8 + 255) / 256 * 256; }
 
-// Columns (a multiple of 8) of one item for heads of D: what the registers hold.
-int most_tiles(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+// The most tiles of 8 columns of one item for heads of D that registers hold without slowing down
+// (D = 128, 32 columns in one item of four tiles and in two of two: 16 sequences of up to 8192 tokens
+// 66 and 62 us, 64 of up to 1000 85 and 69; 24 columns in one of three and in two of two: 38
+// sequences of 8329 tokens 137 and 210 us), and the most columns of all CTAs of an SM.
+int most_tiles(int D) { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+int most_columns(int D) {
+    int n = 0;
+    for (int t = 1; t <= most_tiles(D); ++t) n = std::max(n, 8 * t * ctas_of(D, t));
+    return n;
+}
 
 template <int D, int NT>
 cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
@@ -989,7 +1010,7 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
 
     Launch L{};
     L.sms = c.sms;
-    L.grid = (int64_t)c.sms * kCtasPerSm;
+    L.grid = (int64_t)c.sms * ctas_of(D, NT);
     L.smem = sizeof(Smem<D, NT>);
     int64_t grid = 0;
     auto k = kv4_attention_kernel<D, NT>;
@@ -1025,18 +1046,21 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
 }  // namespace
 
 int64_t kv4_attention_workspace(int seqs, int D, int sms) {
-    const int64_t cols = 8 * most_tiles(D);
-    return prefix_bytes(seqs) + (int64_t)sms * kCtasPerSm * 2 * cols * (D + 2) * 4;
+    return prefix_bytes(seqs) + (int64_t)sms * 2 * most_columns(D) * (D + 2) * 4;
 }
 
 cudaError_t launch_kv4_attention(const Kv4Attention& c, cudaStream_t s) {
-    // the fewest column tiles that hold the queries of one item
-    const int64_t cols = (int64_t)c.max_q * (c.heads / c.kv_heads);
+    // the fewest blocks of columns, and for these the fewest tiles
+    const int64_t cols = (int64_t)c.max_q * (c.heads / c.kv_heads), most = 8 * most_tiles(c.D);
+    const int64_t blocks = (cols + most - 1) / most;
+    const int nt = (int)((cols + 8 * blocks - 1) / (8 * blocks));
     switch (c.D) {
         case 64:
-            return cols <= 8 ? run<64, 1>(c, s) : cols <= 16 ? run<64, 2>(c, s) : run<64, 4>(c, s);
-        case 128: return cols <= 8 ? run<128, 1>(c, s) : run<128, 2>(c, s);
-        case 256: return run<256, 1>(c, s);
+            return nt == 1 ? run<64, 1>(c, s) : nt == 2 ? run<64, 2>(c, s)
+                   : nt == 3 ? run<64, 3>(c, s) : run<64, 4>(c, s);
+        case 128:
+            return nt == 1 ? run<128, 1>(c, s) : nt == 2 ? run<128, 2>(c, s) : run<128, 3>(c, s);
+        case 256: return nt == 1 ? run<256, 1>(c, s) : run<256, 2>(c, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -243,6 +243,17 @@ def test_several_tokens(Hq, Hk, D, max_q):
     check(q, cache, table, lens, cu, max_q)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,n", [(8, 1, 128, 3), (4, 1, 128, 5), (14, 2, 128, 3), (8, 1, 128, 4), (8, 2, 128, 13),
+                                       (8, 1, 64, 3), (10, 2, 64, 4), (8, 1, 64, 5), (8, 1, 256, 2), (3, 1, 256, 3),
+                                       (6, 2, 256, 6)])
+@pytest.mark.parametrize("lens", [[60, 400, 17], [700, 90, 2000]])
+def test_columns_of_every_width(Hq, Hk, D, n, lens):
+    """9 to 52 (query token, head) columns of a kv head: one to several tiles and blocks of them."""
+    cu = [n * i for i in range(len(lens) + 1)]
+    cache, table, g = filled(lens, Hk, 32, D, seed=D + n)
+    check(torch.randn(cu[-1], Hq, D, generator=g).to(BF16), cache, table, lens, cu, max_q=n)
+
+
 @pytest.mark.parametrize("max_q", [1, 4])
 @pytest.mark.parametrize("Hq,Hk,D", [(8, 1, 128), (12, 4, 64), (16, 4, 128), (4, 1, 256)])
 def test_several_tokens_of_long_and_short_sequences(Hq, Hk, D, max_q):
