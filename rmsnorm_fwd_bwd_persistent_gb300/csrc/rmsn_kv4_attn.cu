@@ -39,7 +39,7 @@
 // Where no sequence is longer than 512 tokens no item is split, and the combine has nothing to do;
 // it is not launched where the page table holds no more than that.  Split and whole: one sequence
 // of 16 tokens 8.7 and 6.0 us, 64 of up to 100 11.6 and 8.6, 300 of up to 500 60 and 51, but 64 of
-// up to 1000 23.0 and 23.3, of up to 2000 29.9 and 37.4.
+// up to 1000 23.0 and 23.3, of up to 2000 29.9 and 37.4.  Where such items are many, each is one warp's.
 //
 // Measured on GB300, 32 + 8 heads of 128, replayed from a graph: one sequence of 131072 tokens
 // 40.7 us (floor 24.7), 64 sequences of 500 to 16000 122 us (floor 100); longer caches add 93% of
@@ -64,6 +64,7 @@ constexpr int kUnit = 2 * kKv4Block;  // tokens per unit of work
 constexpr int kMinShare = kWarps;  // least share of a CTA: a unit for each warp
 constexpr int kItemCost = 8;  // what entering and merging an item costs, in units
 constexpr int kWholeUnits = 16;  // no item is split where no sequence is longer
+constexpr int kSoloUnits = 4;    // short enough for a warp to each item as soon as every CTA has one
 
 // CTAs per SM that the registers are divided among, and ring stages of one unit per warp (two are
 // 160 KiB in flight per SM at D = 128 and 256 with four CTAs).
@@ -617,7 +618,8 @@ struct Warp {
     }
 };
 
-template <int D, int NT>
+// SOLO: every item is a warp's own (no sequence is longer than kWholeUnits).
+template <int D, int NT, bool SOLO>
 __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_kernel(const Args a) {
     using Sm = Smem<D, NT>;
     constexpr int S = Sm::S, QC = Sm::QC;
@@ -645,12 +647,15 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         longest = max(longest, s.units);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
-    const bool whole = longest <= kWholeUnits;
+    const bool whole = SOLO || longest <= kWholeUnits;
     if (whole) total = items;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const int64_t per = share_of(total, gridDim.x, whole ? 1 : kMinShare);
-    const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
+    const int first_warp = SOLO ? 0 : warp;
+    constexpr int WARPS = SOLO ? 1 : kWarps;  // that share an item
+    const int64_t per = share_of(total, gridDim.x * (kWarps / WARPS), whole ? 1 : kMinShare);
+    const int64_t begin = (SOLO ? blockIdx.x * kWarps + warp : blockIdx.x) * per;
+    const int64_t end = min(begin + per, total);
     if (begin >= end && blockIdx.x != 0) return;
     int b = 0;
     int64_t seq_first = 0;  // first place of sequence b
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
     bool dead = false;
     // record x & 1 of this warp's unit x / 2; -1: behind the end, or page outside the cache
     auto record = [&](int x) -> int {
-        const int ku = it.k0 + warp + (x >> 1) * kWarps, kb = 2 * ku + (x & 1);
+        const int ku = it.k0 + first_warp + (x >> 1) * WARPS, kb = 2 * ku + (x & 1);
         if (ku >= it.k1 || kb * kKv4Block >= it.s.len) return -1;
         const int p = kb / a.nb;
         const int page = __ldg(a.table + it.b * a.table_stride + p);
@@ -736,7 +741,12 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         }
     };
     auto units_of = [&]() {
-        return dead ? 0 : max(0, (it.k1 - it.k0 - warp + kWarps - 1) / kWarps);
+        return dead ? 0 : max(0, (it.k1 - it.k0 - first_warp + WARPS - 1) / WARPS);
+    };
+
+    auto together = [] {  // the warps that share an item
+        if constexpr (SOLO) __syncwarp();
+        else __syncthreads();
     };
 
     if (!advance(Piece{seq_of<QC>(a, b, false), b, 0, 0, 0, 0, seq_first, begin})) return;
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         // every column sees the tokens before this one
         const int safe = len - s.n + 1 + a.over_group(it.qb * QC);
         st.begin(a, s, it.qb, it.h, lane);
-        int stage = 0, tok0 = (it.k0 + warp) * kUnit;
+        int stage = 0, tok0 = (it.k0 + first_warp) * kUnit;
         for (int i = 0; i < n; ++i) {
             const int got = (have >> (2 * stage)) & 3u;
             if (got) {
@@ -778,7 +788,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
                 next = record(2 * (i + 17) + lane);
             }
             stage = stage + 1 == S ? 0 : stage + 1;
-            tok0 += kWarps * kUnit;
+            tok0 += WARPS * kUnit;
         }
 
         // merge the warps
@@ -817,21 +827,22 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
             for (int i = 0; i < Sm::P; ++i)
                 if (i < n) issue(i, now, i);
         }
-        __syncthreads();
-        for (int x = threadIdx.x; x < QC * D / 4; x += kWarps * 32) {
+        together();
+        for (int x = SOLO ? lane : threadIdx.x; x < QC * D / 4; x += WARPS * 32) {
             const int col = x / (D / 4), e4 = x % (D / 4);
             const int idx = col0 + col;
             if (idx >= cols) continue;
-            float m = sm.m[0][col];
+            const int w0 = SOLO ? warp : 0;
+            float m = sm.m[w0][col];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sm.m[w][col]);
+            for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sm.m[w][col]);
             float l = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float e = ex2(sm.m[w][col] - m);
-                const float4 o = *reinterpret_cast<const float4*>(sm.sums(w, col) + 4 * e4);
-                l = fmaf(e, sm.l[w][col], l);
+            for (int w = 0; w < WARPS; ++w) {
+                const float e = ex2(sm.m[w0 + w][col] - m);
+                const float4 o = *reinterpret_cast<const float4*>(sm.sums(w0 + w, col) + 4 * e4);
+                l = fmaf(e, sm.l[w0 + w][col], l);
                 v.x = fmaf(e, o.x, v.x);
                 v.y = fmaf(e, o.y, v.y);
                 v.z = fmaf(e, o.z, v.z);
@@ -850,7 +861,7 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT)) kv4_attention_ker
         }
         if (!more) break;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring is next
-        __syncthreads();
+        together();
 #pragma unroll
         for (int i = Sm::P; i < S; ++i)
             if (i < n) issue(i, now, i);
@@ -980,7 +991,7 @@ int most_columns(int D) {
     return n;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SOLO>
 cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     Args a{};
     a.q = static_cast<const bf16*>(c.q);
@@ -1013,7 +1024,7 @@ cudaError_t run(const Kv4Attention& c, cudaStream_t s) {
     L.grid = (int64_t)c.sms * ctas_of(D, NT);
     L.smem = sizeof(Smem<D, NT>);
     int64_t grid = 0;
-    auto k = kv4_attention_kernel<D, NT>;
+    auto k = kv4_attention_kernel<D, NT, SOLO>;
     cudaError_t e = fit_grid((const void*)k, L, kWarps * 32, &grid);
     if (e != cudaSuccess) return e;
     uint8_t* ws = static_cast<uint8_t*>(c.ws);
@@ -1049,6 +1060,20 @@ int64_t kv4_attention_workspace(int seqs, int D, int sms) {
     return prefix_bytes(seqs) + (int64_t)sms * 2 * most_columns(D) * (D + 2) * 4;
 }
 
+// Items of short sequences, more than there are CTAs: a warp to each.  It takes an item's units one
+// after the other, but with no barriers and no merge (300 sequences of up to 16 / 100 / 200 tokens
+// 24.2 / 31.1 / 36.0 us with a CTA to each, 12.8 / 17.6 / 23.7 so; with fewer items than CTAs it is
+// slower: one sequence of 100 tokens 6.5 and 10.6).
+template <int D, int NT>
+cudaError_t short_or_long(const Kv4Attention& c, cudaStream_t s) {
+    const int64_t ctas = (int64_t)c.sms * ctas_of(D, NT);
+    const int64_t items = std::max((int64_t)c.seqs * c.kv_heads, (int64_t)c.tokens * c.heads / (8 * NT));
+    const int64_t tokens = (int64_t)c.table_width * c.blocks_per_page * kKv4Block;  // of a sequence, at most
+    const bool solo = tokens <= kWholeUnits * kUnit &&
+                      items > (tokens <= kSoloUnits * kUnit ? ctas : 2 * ctas);
+    return solo ? run<D, NT, true>(c, s) : run<D, NT, false>(c, s);
+}
+
 cudaError_t launch_kv4_attention(const Kv4Attention& c, cudaStream_t s) {
     // the fewest blocks of columns, and for these the fewest tiles
     const int64_t cols = (int64_t)c.max_q * (c.heads / c.kv_heads), most = 8 * most_tiles(c.D);
@@ -1056,11 +1081,12 @@ cudaError_t launch_kv4_attention(const Kv4Attention& c, cudaStream_t s) {
     const int nt = (int)((cols + 8 * blocks - 1) / (8 * blocks));
     switch (c.D) {
         case 64:
-            return nt == 1 ? run<64, 1>(c, s) : nt == 2 ? run<64, 2>(c, s)
-                   : nt == 3 ? run<64, 3>(c, s) : run<64, 4>(c, s);
+            return nt == 1 ? short_or_long<64, 1>(c, s) : nt == 2 ? short_or_long<64, 2>(c, s)
+                   : nt == 3 ? run<64, 3, false>(c, s) : run<64, 4, false>(c, s);
         case 128:
-            return nt == 1 ? run<128, 1>(c, s) : nt == 2 ? run<128, 2>(c, s) : run<128, 3>(c, s);
-        case 256: return nt == 1 ? run<256, 1>(c, s) : run<256, 2>(c, s);
+            return nt == 1 ? short_or_long<128, 1>(c, s) : nt == 2 ? short_or_long<128, 2>(c, s)
+                           : run<128, 3, false>(c, s);
+        case 256: return nt == 1 ? short_or_long<256, 1>(c, s) : run<256, 2, false>(c, s);
         default: return cudaErrorInvalidValue;
     }
 }

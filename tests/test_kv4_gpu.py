@@ -345,6 +345,17 @@ def test_many_sequences():
     check(torch.randn(300, 4, 64, generator=g).to(BF16), cache, table, lens)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,longest,n", [(4, 4, 128, 100, 1), (8, 8, 64, 480, 1), (4, 4, 256, 300, 1),
+                                               (16, 4, 128, 128, 3), (12, 4, 64, 300, 3)])
+def test_more_short_items_than_ctas(Hq, Hk, D, longest, n):
+    """Thousands of short items, some empty, in page tables of at most 512 tokens."""
+    lens = [(i * 53) % (longest + 1) for i in range(420)]
+    cache, table, g = filled(lens, Hk, 32, D, seed=D + n)
+    table = table[:, :-(-longest // 32)].contiguous()
+    cu = [n * i for i in range(len(lens) + 1)]
+    check(torch.randn(cu[-1], Hq, D, generator=g).to(BF16), cache, table, lens, cu if n > 1 else None, max_q=n)
+
+
 @pytest.mark.parametrize("std", [1e-3, 1.0, 40.0])
 @pytest.mark.parametrize("scale", [None, 0.0, -0.3, 3.0])
 def test_score_ranges(std, scale):
