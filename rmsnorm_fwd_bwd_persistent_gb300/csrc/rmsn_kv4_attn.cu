@@ -39,7 +39,8 @@
 // Where no sequence is longer than 512 tokens no item is split, and the combine has nothing to do;
 // it is not launched where the page table holds no more than that.  Split and whole: one sequence
 // of 16 tokens 8.7 and 6.0 us, 64 of up to 100 11.6 and 8.6, 300 of up to 500 60 and 51, but 64 of
-// up to 1000 23.0 and 23.3, of up to 2000 29.9 and 37.4.  Where such items are many, each is one warp's.
+// up to 1000 23.0 and 23.3, of up to 2000 29.9 and 37.4.  Where such items are many, each is one
+// warp's.
 //
 // Measured on GB300, 32 + 8 heads of 128, replayed from a graph: one sequence of 131072 tokens
 // 40.7 us (floor 24.7), 64 sequences of 500 to 16000 122 us (floor 100); longer caches add 93% of
@@ -227,9 +228,9 @@ struct Piece {
 };
 
 // Shared memory of a CTA.  A warp's sums at the end of an item take the place of the last stages
-// of its own ring, which is empty then, and of its q; the first P stages are already filled for the next item
-// meanwhile.  Dims are in the order of the fragments (dim_of), which keeps the stores free of bank
-// conflicts.
+// of its own ring, which is empty then, and of its q; the first P stages are already filled for the
+// next item meanwhile.  Dims are in the order of the fragments (dim_of), which keeps the stores free
+// of bank conflicts.
 template <int D, int NT>
 struct Smem {
     static constexpr int S = stages_of(D, NT);
